@@ -11,8 +11,10 @@ from ._abi import (  # noqa: F401
     COLWISE,
     GEMM_SPLIT_MIN_WORK_DEFAULT,
     MAX_CONTRACTION_FPROP,
+    MAX_NORM_COLS,
     ROWWISE,
     Fp8Error,
+    fp8_add_rmsnorm_quantize_1x128,
     fp8_block_gemm_dgrad,
     fp8_block_gemm_fprop,
     fp8_block_gemm_wgrad,
@@ -27,6 +29,8 @@ from ._abi import (  # noqa: F401
     fp8_last_cuda_error,
     fp8_quantize_act_1x128,
     fp8_quantize_weight_128x128,
+    fp8_rmsnorm_backward,
+    fp8_rmsnorm_backward_workspace_bytes,
     fp8_rmsnorm_quantize_1x128,
     fp8_rmsnorm_rstd,
     fp8_selftest_division,

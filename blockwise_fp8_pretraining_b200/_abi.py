@@ -19,6 +19,7 @@ from . import build as _build
 ROWWISE, COLWISE, BOTH = 1, 2, 3
 MAX_CONTRACTION_FPROP = 32768
 GEMM_SPLIT_MIN_WORK_DEFAULT = 160      # FP8_GEMM_SPLIT_MIN_WORK_DEFAULT
+MAX_NORM_COLS = 16384                  # FP8_MAX_NORM_COLS
 
 _lib = None
 
@@ -61,6 +62,9 @@ def load() -> ctypes.CDLL:
         "fp8_swiglu_quantize_1x128": [p, i64, i64, i32, p, p, p, p, p],
         "fp8_rmsnorm_rstd": [p, i64, i64, ctypes.c_float, p, p],
         "fp8_rmsnorm_quantize_1x128": [p, i64, i64, p, p, i32, p, p, p, p, p],
+        "fp8_add_rmsnorm_quantize_1x128": [p, p, i64, i64, ctypes.c_float, p, i32, p, p, p, p, p, p, p],
+        "fp8_rmsnorm_backward": [p, p, p, p, p, i64, i64, p, p, i32, p, sz, p],
+        "fp8_rmsnorm_backward_workspace_bytes": [i64, i64, p],
         "fp8_selftest_silu_bf16": [p, p],
         "fp8_block_gemm_fprop": [p, p, p, p, p, i64, i64, i64, p, sz, p],
         "fp8_block_gemm_dgrad": [p, p, p, p, p, i64, i64, i64, p, sz, p],
@@ -278,6 +282,99 @@ def fp8_rmsnorm_quantize_1x128(x, rstd, gamma, mode=BOTH, q_row=None, s_row=None
                                           _ptr(s_row), _ptr(q_colT), _ptr(s_col), _stream(stream)),
            "fp8_rmsnorm_quantize_1x128")
     return outs
+
+
+def _alloc(shape, dtype, like, allocated):
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    allocated.append(t)
+    return t
+
+
+def _given(t, dtype, shape, like, allocated, name):
+    """t checked, or a new tensor noted in `allocated`."""
+    return _alloc(shape, dtype, like, allocated) if t is None else _want(t, dtype, shape, name)
+
+
+def fp8_add_rmsnorm_quantize_1x128(x, gamma, residual=None, eps=1e-6, mode=BOTH, sum_out=None, rstd=None, q_row=None,
+                                   s_row=None, q_colT=None, s_col=None, stream=None):
+    """s = bf16(x + residual) (s = x without a residual), RMSNorm of s with
+    the weight gamma, and its output quantized, in one pass.  Returns (s,
+    rstd, q_row, s_row, q_colT, s_col); entries of a grouping the mode leaves
+    out are None, and s is x itself without a residual.  sum_out may be x or
+    residual (in place)."""
+    lib = load()
+    if x.dtype != torch.bfloat16 or x.dim() != 2:
+        raise TypeError("x must be a 2-D bfloat16 tensor")
+    rows, cols = x.shape
+    _want(x, torch.bfloat16, (rows, cols), "x")
+    _want(gamma, torch.bfloat16, (cols,), "gamma")
+    new = []
+    if residual is not None:
+        _want(residual, torch.bfloat16, (rows, cols), "residual")
+        sum_out = _given(sum_out, torch.bfloat16, (rows, cols), x, new, "sum_out")
+    elif sum_out is not None:
+        raise ValueError("sum_out needs a residual: without one the sum is x itself")
+    rstd = _given(rstd, torch.float32, (rows,), x, new, "rstd")
+    if mode & ROWWISE:
+        q_row = _given(q_row, torch.uint8, (rows, cols), x, new, "q_row")
+        s_row = _given(s_row, torch.float32, (cols // 128, rows), x, new, "s_row")
+    else:
+        q_row = s_row = None
+    if mode & COLWISE:
+        q_colT = _given(q_colT, torch.uint8, (cols, rows), x, new, "q_colT")
+        s_col = _given(s_col, torch.float32, (rows // 128, cols), x, new, "s_col")
+    else:
+        q_colT = s_col = None
+    _launch_checks([("x", x), ("residual", residual), ("gamma", gamma), ("sum_out", sum_out), ("rstd", rstd),
+                    ("q_row", q_row), ("s_row", s_row), ("q_colT", q_colT), ("s_col", s_col)], stream)
+    _record(stream, new)
+    _check(lib.fp8_add_rmsnorm_quantize_1x128(_ptr(x), _ptr(residual), rows, cols, float(eps), _ptr(gamma), int(mode),
+                                              _ptr(sum_out), _ptr(rstd), _ptr(q_row), _ptr(s_row), _ptr(q_colT),
+                                              _ptr(s_col), _stream(stream)),
+           "fp8_add_rmsnorm_quantize_1x128")
+    return (x if residual is None else sum_out), rstd, q_row, s_row, q_colT, s_col
+
+
+def fp8_rmsnorm_backward_workspace_bytes(rows: int, cols: int) -> int:
+    """Bytes of scratch fp8_rmsnorm_backward needs on the current device for
+    the gradient of the norm weight (0: none)."""
+    n = ctypes.c_size_t(0)
+    _check(load().fp8_rmsnorm_backward_workspace_bytes(int(rows), int(cols), ctypes.byref(n)),
+           "fp8_rmsnorm_backward_workspace_bytes")
+    return int(n.value)
+
+
+def fp8_rmsnorm_backward(dy, s, rstd, gamma, dresidual=None, ds=None, dgamma=None, accumulate=False, workspace=None,
+                         stream=None):
+    """Gradient through RMSNorm: (ds, dgamma) from dy (the gradient of the
+    norm's output), the norm's input s, its rstd and weight, plus the
+    residual path's gradient of s if there is one.  ds (bf16) may be dy or
+    dresidual (in place); dgamma is float32 [cols], added to with
+    accumulate=True (it must then be given)."""
+    lib = load()
+    if s.dtype != torch.bfloat16 or s.dim() != 2:
+        raise TypeError("s must be a 2-D bfloat16 tensor")
+    rows, cols = s.shape
+    _want(s, torch.bfloat16, (rows, cols), "s")
+    _want(dy, torch.bfloat16, (rows, cols), "dy")
+    _want(rstd, torch.float32, (rows,), "rstd")
+    _want(gamma, torch.bfloat16, (cols,), "gamma")
+    if dresidual is not None:
+        _want(dresidual, torch.bfloat16, (rows, cols), "dresidual")
+    if accumulate and dgamma is None:
+        raise ValueError("accumulate=True needs the dgamma to add to")
+    new = []
+    ds = _given(ds, torch.bfloat16, (rows, cols), s, new, "ds")
+    dgamma = _given(dgamma, torch.float32, (cols,), s, new, "dgamma")
+    _launch_checks([("dy", dy), ("s", s), ("rstd", rstd), ("gamma", gamma), ("dresidual", dresidual), ("ds", ds),
+                    ("dgamma", dgamma), ("workspace", workspace)], stream)
+    if workspace is None:
+        workspace = _alloc((fp8_rmsnorm_backward_workspace_bytes(rows, cols),), torch.uint8, s, new)
+    _record(stream, new)
+    _check(lib.fp8_rmsnorm_backward(_ptr(dy), _ptr(s), _ptr(rstd), _ptr(gamma), _ptr(dresidual), rows, cols, _ptr(ds),
+                                    _ptr(dgamma), int(bool(accumulate)), *_workspace(workspace), _stream(stream)),
+           "fp8_rmsnorm_backward")
+    return ds, dgamma
 
 
 def fp8_quantize_weight_128x128(w, wq=None, sw=None, wqT=None, transposed=True, stream=None):

@@ -11,11 +11,13 @@
 #include <cstring>
 
 #include "../../include/fp8blk.h"
+#include "addnorm.cuh"
 #include "gemm.cuh"
 #include "quantize.cuh"
 
 static_assert(fp8blk::kErrTimeout == static_cast<unsigned int>(FP8_ERR_TIMEOUT),
               "device time-out code must match the C ABI");
+static_assert(fp8blk::addnorm::kMaxCols == FP8_MAX_NORM_COLS, "row length limit must match the C ABI");
 
 namespace {
 
@@ -351,6 +353,111 @@ bool dims_ok_gemm(int64_t M, int64_t N, int64_t K, bool m_positive) {
     return true;
 }
 
+// As launch_pdl, in clusters of `ranks` CTAs.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, unsigned ranks, cudaStream_t stream,
+                               Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ranks;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// add + RMSNorm (+ row-wise quantization when q is given): one launch.
+template <int CPL, int MAX_THREADS>
+cudaError_t launch_norm_rows(const void* x, const void* residual, const void* gamma, int64_t rows, int chunks,
+                             float eps, void* sum_out, float* rstd, uint8_t* q, float* s_row, cudaStream_t stream) {
+    const int wpr = (chunks + 32 * CPL - 1) / (32 * CPL);
+    int teams = MAX_THREADS == 256 ? 8 / wpr : 1;
+    if (teams > rows) teams = static_cast<int>(rows);
+    const unsigned grid = static_cast<unsigned>((rows + teams - 1) / teams);
+    return launch_pdl(addnorm::row_kernel<CPL, MAX_THREADS>, dim3(grid), dim3(32 * wpr * teams), 0, stream,
+                      static_cast<const uint4*>(x), static_cast<const uint4*>(residual),
+                      static_cast<const uint4*>(gamma), rows, chunks, eps, wpr, static_cast<uint4*>(sum_out), rstd,
+                      reinterpret_cast<uint2*>(q), s_row);
+}
+
+fp8_status norm_rows(const void* x, const void* residual, const void* gamma, int64_t rows, int64_t cols, float eps,
+                     void* sum_out, float* rstd, uint8_t* q, float* s_row, cudaStream_t s) {
+    int dev = 0, sms = 0;
+    fp8_status st = current_device(&dev);
+    if (st != FP8_OK) return st;
+    if ((st = sm_count(dev, &sms)) != FP8_OK) return st;
+    const int chunks = static_cast<int>(cols / 8);
+    cudaError_t e;
+    // Few rows: a row over as many warps as it has 512-byte runs, so that a
+    // token's latency is one load and one short pass.  Many rows: up to 64
+    // elements per lane, which leaves the reductions to shuffles.
+    if (rows <= 2 * sms && chunks <= 1024)
+        e = launch_norm_rows<1, 1024>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, s);
+    else if (rows <= 2 * sms)
+        e = launch_norm_rows<2, 1024>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, s);
+    else if (chunks <= 32)
+        e = launch_norm_rows<1, 256>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, s);
+    else if (chunks <= 64)
+        e = launch_norm_rows<2, 256>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, s);
+    else if (chunks <= 128)
+        e = launch_norm_rows<4, 256>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, s);
+    else
+        e = launch_norm_rows<8, 256>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, s);
+    if (e != cudaSuccess) return cuda_fail("add + rmsnorm launch", e);
+    return last_launch_status("add + rmsnorm launch");
+}
+
+template <int TPC>
+fp8_status norm_tiles(const void* x, const void* residual, const void* gamma, int64_t rows, int64_t cols, float eps,
+                      void* sum_out, float* rstd, uint8_t* q_row, float* s_row, uint8_t* q_colT, float* s_col,
+                      cudaStream_t s) {
+    const int tiles = static_cast<int>(cols / 128);
+    const int ranks = (tiles + TPC - 1) / TPC;
+    const cudaError_t e = launch_pdl_cluster(
+        addnorm::tile_kernel<TPC>, dim3(static_cast<unsigned>(rows / 128 * ranks)), dim3(addnorm::kTileThreads),
+        static_cast<unsigned>(ranks), s, static_cast<const __nv_bfloat16*>(x),
+        static_cast<const __nv_bfloat16*>(residual), static_cast<const __nv_bfloat16*>(gamma), rows, cols, eps, ranks,
+        static_cast<__nv_bfloat16*>(sum_out), rstd, q_row, s_row, q_colT, s_col);
+    if (e != cudaSuccess) return cuda_fail("add + rmsnorm tile launch", e);
+    return last_launch_status("add + rmsnorm tile launch");
+}
+
+// Blocks of the norm's gradient: as many as can be resident (two per SM), each
+// of which leaves one row of dgamma's partial sums.
+struct BwdShape {
+    int chunks, cpt, wpr, teams, rows_at_once;
+    unsigned grid;
+};
+BwdShape norm_bwd_shape(int64_t rows, int64_t cols, int sms) {
+    BwdShape b;
+    b.chunks = static_cast<int>(cols / 8);
+    b.cpt = b.chunks <= 256 ? 1 : b.chunks <= 512 ? 2 : b.chunks <= 1024 ? 4 : 8;
+    b.rows_at_once = b.cpt == 1 ? 2 : 1;
+    b.wpr = (b.chunks + 32 * b.cpt - 1) / (32 * b.cpt);
+    b.teams = b.cpt == 1 ? (addnorm::kBwdThreads / 32) / b.wpr : 1;
+    const int64_t per = static_cast<int64_t>(b.teams) * b.rows_at_once;
+    const int64_t need = (rows + per - 1) / per, cap = 2 * static_cast<int64_t>(sms);
+    b.grid = static_cast<unsigned>(need < cap ? need : cap);
+    return b;
+}
+
+template <int CPT, int R>
+cudaError_t launch_norm_bwd(const BwdShape& b, const void* dy, const void* x, const float* rstd, const void* gamma,
+                            const void* dres, int64_t rows, void* ds, float* partial, float* dgamma, int accumulate,
+                            cudaStream_t s) {
+    return launch_pdl(addnorm::bwd_kernel<CPT, R>, dim3(b.grid), dim3(32 * b.wpr * b.teams), 0, s,
+                      static_cast<const uint4*>(dy), static_cast<const uint4*>(x), rstd,
+                      static_cast<const uint4*>(gamma), static_cast<const uint4*>(dres), rows, b.chunks, b.wpr,
+                      static_cast<uint4*>(ds), partial, dgamma, accumulate);
+}
+
 // Scratch of fp8_block_gemm_wgrad_static_ws: the split schedule's workspace
 // as a file-scope device array, for callers that cannot allocate device
 // memory.  Every GPU that loads the library holds it until the process
@@ -462,6 +569,114 @@ fp8_status fp8_rmsnorm_quantize_1x128(const void* x_bf16, int64_t rows, int64_t 
                                                           rstd, gamma_bf16);
     return launch_tile_quant<kTileBoth, kProdNorm>(x_bf16, rows, cols, q_row, s_row, q_colT, s_col, s, rstd,
                                                    gamma_bf16);
+}
+
+fp8_status fp8_add_rmsnorm_quantize_1x128(const void* x_bf16, const void* residual_bf16, int64_t rows, int64_t cols,
+                                          float eps, const void* gamma_bf16, int mode, void* sum_bf16, float* rstd,
+                                          uint8_t* q_row, float* s_row, uint8_t* q_colT, float* s_col, void* stream) {
+    if (mode != FP8_ROWWISE && mode != FP8_COLWISE && mode != FP8_BOTH) return FP8_ERR_MODE;
+    if (rows < 0 || cols < 0 || cols % 128 || rows > kMaxDim || cols > FP8_MAX_NORM_COLS) return FP8_ERR_SHAPE;
+    if ((mode & FP8_COLWISE) && rows % 128) return FP8_ERR_SHAPE;
+    if (!(eps >= 0.0f) || eps > 3.0e38f) return FP8_ERR_SHAPE;
+    if (rows == 0 || cols == 0) return FP8_OK;
+    if (!x_bf16 || !rstd || !gamma_bf16 || (residual_bf16 && !sum_bf16)) return FP8_ERR_NULL;
+    if ((mode & FP8_ROWWISE) && (!q_row || !s_row)) return FP8_ERR_NULL;
+    if ((mode & FP8_COLWISE) && (!q_colT || !s_col)) return FP8_ERR_NULL;
+    if (!aligned16(x_bf16) || !aligned16(rstd) || !aligned16(gamma_bf16) || !aligned16(residual_bf16) ||
+        !aligned16(sum_bf16))
+        return FP8_ERR_ALIGN;
+    if ((mode & FP8_ROWWISE) && (!aligned16(q_row) || !aligned16(s_row))) return FP8_ERR_ALIGN;
+    if ((mode & FP8_COLWISE) && (!aligned16(q_colT) || !aligned16(s_col))) return FP8_ERR_ALIGN;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (mode == FP8_ROWWISE)
+        return norm_rows(x_bf16, residual_bf16, gamma_bf16, rows, cols, eps, sum_bf16, rstd, q_row, s_row, s);
+    if (mode == FP8_COLWISE) q_row = nullptr;
+    if (cols <= 8 * 128)
+        return norm_tiles<1>(x_bf16, residual_bf16, gamma_bf16, rows, cols, eps, sum_bf16, rstd, q_row, s_row, q_colT,
+                             s_col, s);
+    if (cols <= 16 * 128)
+        return norm_tiles<2>(x_bf16, residual_bf16, gamma_bf16, rows, cols, eps, sum_bf16, rstd, q_row, s_row, q_colT,
+                             s_col, s);
+    if (cols <= 32 * 128)
+        return norm_tiles<4>(x_bf16, residual_bf16, gamma_bf16, rows, cols, eps, sum_bf16, rstd, q_row, s_row, q_colT,
+                             s_col, s);
+    // Wider rows do not fit a cluster's registers: the sum and the statistic
+    // first, then the tile quantizer on the sum.
+    const fp8_status st = norm_rows(x_bf16, residual_bf16, gamma_bf16, rows, cols, eps, sum_bf16, rstd, nullptr,
+                                    nullptr, s);
+    if (st != FP8_OK) return st;
+    return fp8_rmsnorm_quantize_1x128(residual_bf16 ? sum_bf16 : x_bf16, rows, cols, rstd, gamma_bf16, mode, q_row,
+                                      s_row, q_colT, s_col, stream);
+}
+
+fp8_status fp8_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols, size_t* bytes) {
+    if (!bytes) return FP8_ERR_NULL;
+    if (rows < 0 || cols < 0 || cols % 128 || rows > kMaxDim || cols > FP8_MAX_NORM_COLS) return FP8_ERR_SHAPE;
+    *bytes = 0;
+    if (rows == 0 || cols == 0) return FP8_OK;
+    int dev = 0, sms = 0;
+    fp8_status st = current_device(&dev);
+    if (st != FP8_OK) return st;
+    if ((st = sm_count(dev, &sms)) != FP8_OK) return st;
+    const BwdShape b = norm_bwd_shape(rows, cols, sms);
+    if (b.grid > 1) *bytes = static_cast<size_t>(b.grid) * static_cast<size_t>(cols) * sizeof(float);
+    return FP8_OK;
+}
+
+fp8_status fp8_rmsnorm_backward(const void* dy_bf16, const void* s_bf16, const float* rstd, const void* gamma_bf16,
+                                const void* dresidual_bf16, int64_t rows, int64_t cols, void* ds_bf16,
+                                float* dgamma_f32, int accumulate, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+    if (accumulate != 0 && accumulate != 1) return FP8_ERR_MODE;
+    if (rows < 0 || cols < 0 || cols % 128 || rows > kMaxDim || cols > FP8_MAX_NORM_COLS) return FP8_ERR_SHAPE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (cols == 0) return FP8_OK;
+    if (!aligned16(dgamma_f32) || !aligned16(workspace)) return FP8_ERR_ALIGN;
+    if (rows == 0) {                   // the sum over no rows
+        if (dgamma_f32 && !accumulate) {
+            const cudaError_t e = cudaMemsetAsync(dgamma_f32, 0, static_cast<size_t>(cols) * sizeof(float), s);
+            if (e != cudaSuccess) return cuda_fail("cudaMemsetAsync(dgamma)", e);
+        }
+        return FP8_OK;
+    }
+    if (!dy_bf16 || !s_bf16 || !rstd || !gamma_bf16 || !ds_bf16) return FP8_ERR_NULL;
+    if (!aligned16(dy_bf16) || !aligned16(s_bf16) || !aligned16(rstd) || !aligned16(gamma_bf16) ||
+        !aligned16(dresidual_bf16) || !aligned16(ds_bf16))
+        return FP8_ERR_ALIGN;
+    int dev = 0, sms = 0;
+    fp8_status st = current_device(&dev);
+    if (st != FP8_OK) return st;
+    if ((st = sm_count(dev, &sms)) != FP8_OK) return st;
+    const BwdShape b = norm_bwd_shape(rows, cols, sms);
+    if (dgamma_f32 && b.grid > 1) {
+        if (!workspace) return FP8_ERR_NULL;
+        if (workspace_bytes < static_cast<size_t>(b.grid) * static_cast<size_t>(cols) * sizeof(float))
+            return FP8_ERR_SHAPE;
+    }
+    float* partial = static_cast<float*>(workspace);
+    cudaError_t e;
+    if (b.cpt == 1)
+        e = launch_norm_bwd<1, 2>(b, dy_bf16, s_bf16, rstd, gamma_bf16, dresidual_bf16, rows, ds_bf16, partial,
+                                  dgamma_f32, accumulate, s);
+    else if (b.cpt == 2)
+        e = launch_norm_bwd<2, 1>(b, dy_bf16, s_bf16, rstd, gamma_bf16, dresidual_bf16, rows, ds_bf16, partial,
+                                  dgamma_f32, accumulate, s);
+    else if (b.cpt == 4)
+        e = launch_norm_bwd<4, 1>(b, dy_bf16, s_bf16, rstd, gamma_bf16, dresidual_bf16, rows, ds_bf16, partial,
+                                  dgamma_f32, accumulate, s);
+    else
+        e = launch_norm_bwd<8, 1>(b, dy_bf16, s_bf16, rstd, gamma_bf16, dresidual_bf16, rows, ds_bf16, partial,
+                                  dgamma_f32, accumulate, s);
+    if (e != cudaSuccess) return cuda_fail("rmsnorm backward launch", e);
+    if ((st = last_launch_status("rmsnorm backward launch")) != FP8_OK) return st;
+    if (dgamma_f32 && b.grid > 1) {
+        e = launch_pdl(addnorm::dgamma_kernel, dim3(static_cast<unsigned>(cols / 32)), dim3(256), 0, s,
+                       static_cast<const float*>(partial), static_cast<int>(b.grid), static_cast<int>(cols),
+                       dgamma_f32, accumulate);
+        if (e != cudaSuccess) return cuda_fail("dgamma launch", e);
+        return last_launch_status("dgamma launch");
+    }
+    return FP8_OK;
 }
 
 fp8_status fp8_quantize_weight_128x128(const void* w_bf16, int64_t n, int64_t k, uint8_t* wq,

@@ -210,6 +210,71 @@ fp8_status fp8_rmsnorm_quantize_1x128(const void *x_bf16, int64_t rows, int64_t 
                                       uint8_t *q_row, float *s_row, uint8_t *q_colT,
                                       float *s_col, void *stream);
 
+/* Longest row fp8_add_rmsnorm_quantize_1x128 and fp8_rmsnorm_backward take. */
+#define FP8_MAX_NORM_COLS 16384
+
+/*
+ * Residual addition, RMSNorm and quantization in one pass over the data:
+ * s = bf16(x + residual) (one rounding to nearest even), rstd and y as in
+ * fp8_rmsnorm_rstd and fp8_rmsnorm_quantize_1x128 of s, and the codes and
+ * scales of y.  Given the rstd it writes, the codes and scales equal those of
+ * fp8_rmsnorm_quantize_1x128 on s bit for bit.  Non-finite inputs are outside
+ * the definition.  Passage: as fp8_rmsnorm_quantize_1x128; the blocks of the
+ * Qwen3-1.7B configuration add their input to a residual stream and
+ * normalize the sum.
+ *
+ *   x_bf16        [rows, cols] bf16.
+ *   residual_bf16 [rows, cols] bf16, or NULL for s = x.
+ *   rows >= 0; a multiple of 128 when mode includes FP8_COLWISE (any number,
+ *              one token included, with FP8_ROWWISE).
+ *   cols >= 0, a multiple of 128, <= FP8_MAX_NORM_COLS.
+ *   eps  >= 0, finite.
+ *   gamma_bf16    [cols] bf16 norm weight.
+ *   sum_bf16      [rows, cols] bf16, receives s; may be x_bf16 or
+ *              residual_bf16 itself (in place).  Not written, and may be
+ *              NULL, when residual_bf16 is NULL.
+ *   rstd [rows] f32, written.
+ *   mode, q_row, s_row, q_colT, s_col: as fp8_quantize_act_1x128.
+ * All pointers used are 16-byte aligned.  rows == 0 or cols == 0 is a no-op
+ * (pointers may then be NULL).
+ */
+fp8_status fp8_add_rmsnorm_quantize_1x128(const void *x_bf16, const void *residual_bf16, int64_t rows,
+                                          int64_t cols, float eps, const void *gamma_bf16, int mode,
+                                          void *sum_bf16, float *rstd, uint8_t *q_row, float *s_row,
+                                          uint8_t *q_colT, float *s_col, void *stream);
+
+/*
+ * Gradient through RMSNorm, joined by the residual path's: with n = s rstd
+ * and g = gamma dy (FP32; the forward pass's roundings are passed straight
+ * through, and rstd is differentiated as the function of s it is),
+ *   ds     = bf16(rstd (g - n mean_k(g n)) + dresidual)
+ *   dgamma = sum over rows of dy n, FP32 (stored, or added to what is there).
+ * ds is the gradient of both x and residual of s = x + residual.  Sums are
+ * FP32 in a fixed order, so results repeat run to run.  Passage: as
+ * fp8_add_rmsnorm_quantize_1x128, and the training-setup paragraph
+ * (activations in BF16, master state in FP32).
+ *
+ *   dy_bf16 [rows, cols] bf16, the gradient of y; s_bf16 [rows, cols] bf16;
+ *   rstd [rows] f32; gamma_bf16 [cols] bf16;
+ *   dresidual_bf16 [rows, cols] bf16, or NULL for none.
+ *   rows >= 0; cols >= 0, a multiple of 128, <= FP8_MAX_NORM_COLS.
+ *   ds_bf16 [rows, cols] bf16, written; may be dy_bf16 or dresidual_bf16.
+ *   dgamma_f32 [cols] f32, or NULL to leave it out; accumulate = 0: written,
+ *           1: added to (FP8_ERR_MODE for other values).
+ *   workspace: workspace_bytes >= fp8_rmsnorm_backward_workspace_bytes(rows,
+ *           cols) of scratch, needed only for dgamma (the size may be 0); its
+ *           contents before the call do not matter.  Two calls that may run
+ *           at the same time need different workspaces.  Too small a one is
+ *           FP8_ERR_SHAPE.
+ * All pointers used are 16-byte aligned.  cols == 0 is a no-op; rows == 0
+ * writes dgamma = 0 (unless accumulating) and nothing else.
+ */
+fp8_status fp8_rmsnorm_backward(const void *dy_bf16, const void *s_bf16, const float *rstd,
+                                const void *gamma_bf16, const void *dresidual_bf16, int64_t rows,
+                                int64_t cols, void *ds_bf16, float *dgamma_f32, int accumulate,
+                                void *workspace, size_t workspace_bytes, void *stream);
+fp8_status fp8_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols, size_t *bytes);
+
 /*
  * Weight quantizer, 128x128 blocks.
  * Passage: Puro-2B-Base model card, training-setup paragraph (blockwise E4M3);

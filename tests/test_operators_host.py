@@ -1,0 +1,86 @@
+"""Refusals and marshalling of the operators around the linears, without a
+GPU: bad arguments come back as a status before anything is launched (the fake
+pointers are never dereferenced)."""
+import ctypes
+
+import pytest
+import torch
+
+import blockwise_fp8_pretraining_b200 as fp8
+
+OK, NULL, SHAPE, ALIGN, MODE = 0, 1, 2, 3, 4
+A16, MIS = 0x10000, 0x10008
+S = ctypes.c_void_p(0)
+
+
+def P(v):
+    return ctypes.c_void_p(v)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from blockwise_fp8_pretraining_b200 import build
+
+    build.build()
+    return fp8.load()
+
+
+def test_limits_match_the_header():
+    import re
+
+    from blockwise_fp8_pretraining_b200 import build
+
+    defines = dict(re.findall(r"#define\s+(FP8_\w+)\s+(\d+)", open(build.HEADER).read()))
+    assert int(defines["FP8_MAX_NORM_COLS"]) == fp8.MAX_NORM_COLS
+
+
+def test_add_rmsnorm_quantize_rejections(lib):
+    def call(x=A16, res=A16, rows=256, cols=256, eps=1e-6, gamma=A16, mode=3, s=A16, r=A16, qr=A16, sr=A16, qc=A16,
+             sc=A16):
+        return lib.fp8_add_rmsnorm_quantize_1x128(P(x), P(res), rows, cols, eps, P(gamma), mode, P(s), P(r), P(qr),
+                                                  P(sr), P(qc), P(sc), S)
+
+    for mode in (0, 4, -1):
+        assert call(mode=mode) == MODE
+    assert call(cols=200) == SHAPE
+    assert call(cols=fp8.MAX_NORM_COLS + 128) == SHAPE
+    assert call(rows=-1) == SHAPE
+    assert call(rows=100) == SHAPE and call(rows=100, mode=2) == SHAPE     # groups along tokens need 128
+    assert call(eps=-1.0) == SHAPE and call(eps=float("nan")) == SHAPE and call(eps=float("inf")) == SHAPE
+    for name in ("x", "gamma", "s", "r", "qr", "sr", "qc", "sc"):
+        assert call(**{name: None}) == NULL, name
+        assert call(**{name: MIS}) == ALIGN, name
+    assert call(res=MIS) == ALIGN
+    assert call(rows=0, x=None) == OK and call(cols=0, x=None) == OK
+
+
+def test_rmsnorm_backward_rejections(lib):
+    def call(dy=A16, s=A16, r=A16, g=A16, e=A16, rows=256, cols=256, ds=A16, dg=A16, acc=0, ws=A16, n=1 << 30):
+        return lib.fp8_rmsnorm_backward(P(dy), P(s), P(r), P(g), P(e), rows, cols, P(ds), P(dg), acc, P(ws), n, S)
+
+    assert call(acc=2) == MODE
+    assert call(cols=100) == SHAPE and call(rows=-1) == SHAPE and call(cols=fp8.MAX_NORM_COLS + 128) == SHAPE
+    for name in ("dy", "s", "r", "g", "ds"):
+        assert call(**{name: None}) == NULL, name
+        assert call(**{name: MIS}) == ALIGN, name
+    for name in ("e", "dg", "ws"):
+        assert call(**{name: MIS}) == ALIGN, name
+    assert call(cols=0, dy=None) == OK
+    assert call(rows=0, dy=None, dg=None) == OK
+    assert lib.fp8_rmsnorm_backward_workspace_bytes(128, 128, None) == NULL
+    n = ctypes.c_size_t(7)
+    assert lib.fp8_rmsnorm_backward_workspace_bytes(128, 100, ctypes.byref(n)) == SHAPE
+    assert lib.fp8_rmsnorm_backward_workspace_bytes(0, 128, ctypes.byref(n)) == OK and n.value == 0
+
+
+def test_binding_refuses_before_the_library(lib):
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    g = torch.zeros(256, dtype=torch.bfloat16)
+    with pytest.raises(TypeError):
+        fp8.fp8_add_rmsnorm_quantize_1x128(x.float(), g)
+    with pytest.raises(ValueError):                  # not on a GPU
+        fp8.fp8_add_rmsnorm_quantize_1x128(x, g)
+    with pytest.raises(TypeError):
+        fp8.fp8_rmsnorm_backward(x, x.float(), torch.zeros(4), g)
+    with pytest.raises(ValueError):
+        fp8.fp8_rmsnorm_backward(x, x, torch.zeros(4), g)

@@ -12,6 +12,7 @@ from ._abi import (  # noqa: F401
     GEMM_SPLIT_MIN_WORK_DEFAULT,
     MAX_CONTRACTION_FPROP,
     MAX_NORM_COLS,
+    MAX_TOPK,
     ROWWISE,
     Fp8Error,
     fp8_add_rmsnorm_quantize_1x128,
@@ -42,6 +43,8 @@ from ._abi import (  # noqa: F401
     fp8_set_wait_timeout_ns,
     fp8_status_string,
     fp8_swiglu_quantize_1x128,
+    fp8_token_logprobs,
+    fp8_token_logprobs_backward,
     exchange_shards,
     header_functions,
     lib_path,

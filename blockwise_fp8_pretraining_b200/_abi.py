@@ -20,6 +20,7 @@ ROWWISE, COLWISE, BOTH = 1, 2, 3
 MAX_CONTRACTION_FPROP = 32768
 GEMM_SPLIT_MIN_WORK_DEFAULT = 160      # FP8_GEMM_SPLIT_MIN_WORK_DEFAULT
 MAX_NORM_COLS = 16384                  # FP8_MAX_NORM_COLS
+MAX_TOPK = 32                          # FP8_MAX_TOPK
 
 _lib = None
 
@@ -65,6 +66,8 @@ def load() -> ctypes.CDLL:
         "fp8_add_rmsnorm_quantize_1x128": [p, p, i64, i64, ctypes.c_float, p, i32, p, p, p, p, p, p, p],
         "fp8_rmsnorm_backward": [p, p, p, p, p, i64, i64, p, p, i32, p, sz, p],
         "fp8_rmsnorm_backward_workspace_bytes": [i64, i64, p],
+        "fp8_token_logprobs": [p, i32, i64, i64, i64, p, i32, p, p, p, p, p, p],
+        "fp8_token_logprobs_backward": [p, i32, i64, i64, i64, p, p, p, p, p, p, i64, p],
         "fp8_selftest_silu_bf16": [p, p],
         "fp8_block_gemm_fprop": [p, p, p, p, p, i64, i64, i64, p, sz, p],
         "fp8_block_gemm_dgrad": [p, p, p, p, p, i64, i64, i64, p, sz, p],
@@ -375,6 +378,93 @@ def fp8_rmsnorm_backward(dy, s, rstd, gamma, dresidual=None, ds=None, dgamma=Non
                                     _ptr(dgamma), int(bool(accumulate)), *_workspace(workspace), _stream(stream)),
            "fp8_rmsnorm_backward")
     return ds, dgamma
+
+
+_DTYPES = {torch.bfloat16: 0, torch.float32: 1}      # FP8_BF16, FP8_F32
+
+
+def _logits(t, name, like=None):
+    """(dtype code, row stride) of a 2-D bf16 or float32 CUDA tensor whose
+    rows are contiguous (a view into a padded vocabulary will do)."""
+    if t.dim() != 2 or t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be a 2-D bfloat16 or float32 tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if like is not None and (t.dtype != like.dtype or t.shape != like.shape):
+        raise ValueError(f"{name}: expected {like.dtype} {tuple(like.shape)}, got {t.dtype} {tuple(t.shape)}")
+    rows, vocab = t.shape
+    ld = t.stride(0) if rows > 1 else max(vocab, t.stride(0))
+    if (vocab > 1 and t.stride(1) != 1) or ld < vocab:
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap")
+    return _DTYPES[t.dtype], ld
+
+
+def fp8_token_logprobs(logits, targets=None, topk=0, logprob=None, entropy=None, stats=None, top_logprob=None,
+                       top_index=None, stream=None):
+    """Log probability of each row's target token (int64 [rows]; negative:
+    none), the entropy of each row's distribution, stats [rows, 2] (the row's
+    maximum m and log sum exp(x - m)), and the topk most likely tokens (log
+    probabilities and int64 indices [rows, topk], largest first, equal logits
+    by index) of bf16 or float32 logits [rows, vocab].  Returns (logprob,
+    entropy, stats, top_logprob, top_index); logprob is None without targets,
+    the last two with topk = 0."""
+    lib = load()
+    code, ld = _logits(logits, "logits")
+    rows, vocab = logits.shape
+    new = []
+    if targets is not None:
+        _want(targets, torch.int64, (rows,), "targets")
+        logprob = _given(logprob, torch.float32, (rows,), logits, new, "logprob")
+    else:
+        logprob = None
+    entropy = _given(entropy, torch.float32, (rows,), logits, new, "entropy")
+    stats = _given(stats, torch.float32, (rows, 2), logits, new, "stats")
+    if topk:
+        top_logprob = _given(top_logprob, torch.float32, (rows, topk), logits, new, "top_logprob")
+        top_index = _given(top_index, torch.int64, (rows, topk), logits, new, "top_index")
+    else:
+        top_logprob = top_index = None
+    _launch_checks([("logits", logits), ("targets", targets), ("logprob", logprob), ("entropy", entropy),
+                    ("stats", stats), ("top_logprob", top_logprob), ("top_index", top_index)], stream)
+    _record(stream, new)
+    _check(lib.fp8_token_logprobs(_ptr(logits), code, rows, vocab, ld, _ptr(targets), int(topk), _ptr(logprob),
+                                  _ptr(entropy), _ptr(stats), _ptr(top_logprob), _ptr(top_index), _stream(stream)),
+           "fp8_token_logprobs")
+    return logprob, entropy, stats, top_logprob, top_index
+
+
+def fp8_token_logprobs_backward(logits, targets, stats, dlogprob=None, entropy=None, dentropy=None, dlogits=None,
+                                stream=None):
+    """Gradient of the logits from the gradients of fp8_token_logprobs's
+    logprob and entropy (float32 [rows], either None); entropy is needed with
+    dentropy.  dlogits (the logits' type) may be the logits themselves."""
+    lib = load()
+    code, ld = _logits(logits, "logits")
+    rows, vocab = logits.shape
+    _want(stats, torch.float32, (rows, 2), "stats")
+    if dlogprob is not None:
+        if targets is None:
+            raise ValueError("dlogprob needs targets")
+        _want(dlogprob, torch.float32, (rows,), "dlogprob")
+    if targets is not None:
+        _want(targets, torch.int64, (rows,), "targets")
+    if dentropy is not None:
+        if entropy is None:
+            raise ValueError("dentropy needs the entropy")
+        _want(dentropy, torch.float32, (rows,), "dentropy")
+        _want(entropy, torch.float32, (rows,), "entropy")
+    new = []
+    if dlogits is None:
+        dlogits = _alloc((rows, vocab), logits.dtype, logits, new)
+    _, ld_out = _logits(dlogits, "dlogits", logits)
+    _launch_checks([("logits", logits), ("targets", targets), ("stats", stats), ("dlogprob", dlogprob),
+                    ("entropy", entropy), ("dentropy", dentropy), ("dlogits", dlogits)], stream)
+    _record(stream, new)
+    _check(lib.fp8_token_logprobs_backward(_ptr(logits), code, rows, vocab, ld, _ptr(targets), _ptr(stats),
+                                           _ptr(dlogprob), _ptr(entropy), _ptr(dentropy), _ptr(dlogits), ld_out,
+                                           _stream(stream)),
+           "fp8_token_logprobs_backward")
+    return dlogits
 
 
 def fp8_quantize_weight_128x128(w, wq=None, sw=None, wqT=None, transposed=True, stream=None):

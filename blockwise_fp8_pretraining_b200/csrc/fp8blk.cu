@@ -13,10 +13,12 @@
 #include "../../include/fp8blk.h"
 #include "addnorm.cuh"
 #include "gemm.cuh"
+#include "logprobs.cuh"
 #include "quantize.cuh"
 
 static_assert(fp8blk::kErrTimeout == static_cast<unsigned int>(FP8_ERR_TIMEOUT),
               "device time-out code must match the C ABI");
+static_assert(fp8blk::logp::kMaxTopK == FP8_MAX_TOPK, "alternatives limit must match the C ABI");
 static_assert(fp8blk::addnorm::kMaxCols == FP8_MAX_NORM_COLS, "row length limit must match the C ABI");
 
 namespace {
@@ -61,6 +63,7 @@ std::atomic<int> g_gemm_attr_done[kMaxDevices];
 std::atomic<int> g_gemm_pairs[kMaxDevices][12];  // co-resident CTA pairs per kernel variant
 
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxLd = int64_t(1) << 40;     // row strides; rows * stride stays far inside 64 bits
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -458,6 +461,62 @@ cudaError_t launch_norm_bwd(const BwdShape& b, const void* dy, const void* x, co
                       static_cast<uint4*>(ds), partial, dgamma, accumulate);
 }
 
+// Power of two >= v, within [lo, hi] (both powers of two).
+inline int pow2_between(int64_t v, int lo, int hi) {
+    int p = lo;
+    while (p < hi && p < v) p *= 2;
+    return p;
+}
+
+bool dtype_ok(int dtype) { return dtype == FP8_BF16 || dtype == FP8_F32; }
+bool element_aligned(const void* p, int dtype) {
+    return (reinterpret_cast<uintptr_t>(p) & (dtype == FP8_BF16 ? 1u : 3u)) == 0;
+}
+
+// A row of logits over `ranks` CTAs of `threads` threads: rows are split until
+// the GPU's SMs have several CTAs each (their reductions then hide behind
+// others' loads) as long as every CTA still has 16 KB of the row; a thread has
+// at least one batch of 16-byte vectors.
+template <typename T>
+fp8_status launch_logp(const void* logits, int64_t rows, int64_t vocab, int64_t ld, const int64_t* targets, int topk,
+                       float* logprob, float* entropy, float* stats, float* top_logprob, int64_t* top_index,
+                       cudaStream_t s) {
+    int dev = 0, sms = 0;
+    fp8_status st = current_device(&dev);
+    if (st != FP8_OK) return st;
+    if ((st = sm_count(dev, &sms)) != FP8_OK) return st;
+    const int64_t bytes = vocab * static_cast<int64_t>(sizeof(T));
+    int ranks = 1;
+    while (ranks < logp::kMaxRanks && rows * ranks < 8 * static_cast<int64_t>(sms) && bytes / (2 * ranks) >= 16384)
+        ranks *= 2;
+    const int threads = pow2_between(bytes / ranks / (16 * logp::kBatch), 32, logp::kMaxThreads);
+    if (rows > kMaxDim / ranks) return FP8_ERR_SHAPE;
+    auto kernel = topk ? logp::forward_kernel<T, true> : logp::forward_kernel<T, false>;
+    const cudaError_t e = launch_pdl_cluster(
+        kernel, dim3(static_cast<unsigned>(rows * ranks)), dim3(static_cast<unsigned>(threads)),
+        static_cast<unsigned>(ranks), s, static_cast<const T*>(logits), vocab, ld, targets, topk, ranks, logprob,
+        entropy, reinterpret_cast<float2*>(stats), top_logprob, top_index);
+    if (e != cudaSuccess) return cuda_fail("token log probabilities launch", e);
+    return last_launch_status("token log probabilities launch");
+}
+
+template <typename T>
+fp8_status launch_logp_bwd(const void* logits, int64_t rows, int64_t vocab, int64_t ld, const int64_t* targets,
+                           const float* stats, const float* dlogprob, const float* entropy, const float* dentropy,
+                           void* dlogits, int64_t ld_out, cudaStream_t s) {
+    const int64_t nvec = vocab / logp::Elem<T>::N;
+    const int threads = pow2_between((nvec + logp::kBatch - 1) / logp::kBatch, 32, logp::kMaxThreads);
+    const int64_t per = static_cast<int64_t>(threads) * logp::kBatch;
+    const int64_t chunks = nvec > per ? (nvec + per - 1) / per : 1;
+    if (rows > kMaxDim / chunks) return FP8_ERR_SHAPE;
+    const cudaError_t e = launch_pdl(logp::backward_kernel<T>, dim3(static_cast<unsigned>(rows * chunks)),
+                                     dim3(static_cast<unsigned>(threads)), 0, s, static_cast<const T*>(logits), vocab,
+                                     ld, targets, reinterpret_cast<const float2*>(stats), dlogprob, entropy, dentropy,
+                                     chunks, static_cast<T*>(dlogits), ld_out);
+    if (e != cudaSuccess) return cuda_fail("token log probabilities gradient launch", e);
+    return last_launch_status("token log probabilities gradient launch");
+}
+
 // Scratch of fp8_block_gemm_wgrad_static_ws: the split schedule's workspace
 // as a file-scope device array, for callers that cannot allocate device
 // memory.  Every GPU that loads the library holds it until the process
@@ -677,6 +736,47 @@ fp8_status fp8_rmsnorm_backward(const void* dy_bf16, const void* s_bf16, const f
         return last_launch_status("dgamma launch");
     }
     return FP8_OK;
+}
+
+fp8_status fp8_token_logprobs(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                              const int64_t* targets, int topk, float* logprob, float* entropy, float* stats,
+                              float* top_logprob, int64_t* top_index, void* stream) {
+    if (!dtype_ok(dtype)) return FP8_ERR_MODE;
+    if (rows < 0 || vocab < 1 || ld < vocab || rows > kMaxDim || vocab > kMaxDim || ld > kMaxLd) return FP8_ERR_SHAPE;
+    if (topk < 0 || topk > FP8_MAX_TOPK || topk > vocab) return FP8_ERR_SHAPE;
+    if (rows == 0) return FP8_OK;
+    if (!logits || !stats || (logprob && !targets) || (topk && (!top_logprob || !top_index))) return FP8_ERR_NULL;
+    if (!element_aligned(logits, dtype) || !aligned16(targets) || !aligned16(logprob) || !aligned16(entropy) ||
+        !aligned16(stats) || !aligned16(top_logprob) || !aligned16(top_index))
+        return FP8_ERR_ALIGN;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dtype == FP8_BF16)
+        return launch_logp<__nv_bfloat16>(logits, rows, vocab, ld, targets, topk, logprob, entropy, stats, top_logprob,
+                                          top_index, s);
+    return launch_logp<float>(logits, rows, vocab, ld, targets, topk, logprob, entropy, stats, top_logprob, top_index,
+                              s);
+}
+
+fp8_status fp8_token_logprobs_backward(const void* logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                                       const int64_t* targets, const float* stats, const float* dlogprob,
+                                       const float* entropy, const float* dentropy, void* dlogits, int64_t ld_out,
+                                       void* stream) {
+    if (!dtype_ok(dtype)) return FP8_ERR_MODE;
+    if (rows < 0 || vocab < 1 || ld < vocab || ld_out < vocab || rows > kMaxDim || vocab > kMaxDim || ld > kMaxLd ||
+        ld_out > kMaxLd)
+        return FP8_ERR_SHAPE;
+    if (rows == 0) return FP8_OK;
+    if (!logits || !stats || !dlogits || (dlogprob && !targets) || (dentropy && !entropy)) return FP8_ERR_NULL;
+    if (!element_aligned(logits, dtype) || !element_aligned(dlogits, dtype) || !aligned16(targets) ||
+        !aligned16(stats) || !aligned16(dlogprob) || !aligned16(entropy) || !aligned16(dentropy))
+        return FP8_ERR_ALIGN;
+    if (logits == dlogits && ld != ld_out) return FP8_ERR_SHAPE;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dtype == FP8_BF16)
+        return launch_logp_bwd<__nv_bfloat16>(logits, rows, vocab, ld, targets, stats, dlogprob, entropy, dentropy,
+                                              dlogits, ld_out, s);
+    return launch_logp_bwd<float>(logits, rows, vocab, ld, targets, stats, dlogprob, entropy, dentropy, dlogits,
+                                  ld_out, s);
 }
 
 fp8_status fp8_quantize_weight_128x128(const void* w_bf16, int64_t n, int64_t k, uint8_t* wq,

@@ -275,6 +275,71 @@ fp8_status fp8_rmsnorm_backward(const void *dy_bf16, const void *s_bf16, const f
                                 void *workspace, size_t workspace_bytes, void *stream);
 fp8_status fp8_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols, size_t *bytes);
 
+/* Element types of logits and gradients. */
+enum {
+    FP8_BF16 = 0,
+    FP8_F32 = 1
+};
+
+/* Most alternatives fp8_token_logprobs reports per row. */
+#define FP8_MAX_TOPK 32
+
+/*
+ * Log probabilities of given tokens, the distribution's entropy and its most
+ * likely tokens, from one read of the logits.  Per row x, with m = max x and
+ * L = log(sum_v exp(x_v - m)):
+ *   logprob     = x[target] - m - L; 0 for a negative target (a position
+ *                 without one), NaN for a target >= vocab
+ *   entropy     = -sum_v p_v log p_v, p_v = exp(x_v - m - L)
+ *   stats       = (m, L): m + L is the log of the normalizer
+ *   top_logprob, top_index: the topk largest logits, largest first, equal
+ *                 logits by increasing index; top_logprob = x - m - L
+ * A logit of -inf has probability 0 and adds nothing to the entropy; a row of
+ * nothing else gets stats (-inf, 0), entropy 0 and log probabilities -inf.  A
+ * NaN or +inf logit makes the row's results NaN; NaN logits are never among
+ * the alternatives (where too few others are left, index -1 and NaN).
+ * Arithmetic is FP32 in a fixed order, so results repeat run to run.
+ * Passage: Puro-2B-Base model card (friendli.ai), model property table
+ * (vocabulary of 151,936, untied output embedding) and training-setup
+ * paragraph (operations other than the linears' products in BF16 or FP32).
+ *
+ *   logits  dtype (FP8_BF16 or FP8_F32; FP8_ERR_MODE otherwise), row i at
+ *           logits + i * ld elements, ld >= vocab (a padded vocabulary's
+ *           padding is not read); any alignment of the element type.
+ *   rows >= 0; 1 <= vocab < 2^31; 0 <= topk <= FP8_MAX_TOPK, topk <= vocab.
+ *   targets [rows] int64; may be NULL when logprob is.
+ *   logprob [rows], entropy [rows] f32; either may be NULL.
+ *   stats   [rows, 2] f32.
+ *   top_logprob [rows, topk] f32, top_index [rows, topk] int64; may be NULL
+ *           when topk is 0.
+ * All pointers but logits are 16-byte aligned.  rows == 0 is a no-op.
+ */
+fp8_status fp8_token_logprobs(const void *logits, int dtype, int64_t rows, int64_t vocab, int64_t ld,
+                              const int64_t *targets, int topk, float *logprob, float *entropy,
+                              float *stats, float *top_logprob, int64_t *top_index, void *stream);
+
+/*
+ * Gradient of the logits: with p = exp(x - m - L) from stats,
+ *   dlogits_v = dlogprob (1[v = target] - p_v) - dentropy p_v (log p_v + entropy)
+ * in FP32, rounded once to the logits' type.  A row without a target (negative)
+ * takes no part of dlogprob; a target >= vocab makes the row NaN.
+ *
+ *   logits, dtype, rows, vocab, ld, targets: as fp8_token_logprobs; targets may
+ *           be NULL when dlogprob is.
+ *   stats   [rows, 2] f32 from fp8_token_logprobs.
+ *   dlogprob [rows] f32, or NULL for none.
+ *   entropy [rows] f32 (from fp8_token_logprobs) and dentropy [rows] f32, or
+ *           dentropy NULL for none (entropy is then not read).
+ *   dlogits the same type, row i at dlogits + i * ld_out elements, ld_out >=
+ *           vocab; may be logits itself with ld_out == ld (in place).  Columns
+ *           behind vocab are left as they are.
+ */
+fp8_status fp8_token_logprobs_backward(const void *logits, int dtype, int64_t rows, int64_t vocab,
+                                       int64_t ld, const int64_t *targets, const float *stats,
+                                       const float *dlogprob, const float *entropy,
+                                       const float *dentropy, void *dlogits, int64_t ld_out,
+                                       void *stream);
+
 /*
  * Weight quantizer, 128x128 blocks.
  * Passage: Puro-2B-Base model card, training-setup paragraph (blockwise E4M3);

@@ -32,6 +32,7 @@ def test_limits_match_the_header():
 
     defines = dict(re.findall(r"#define\s+(FP8_\w+)\s+(\d+)", open(build.HEADER).read()))
     assert int(defines["FP8_MAX_NORM_COLS"]) == fp8.MAX_NORM_COLS
+    assert int(defines["FP8_MAX_TOPK"]) == fp8.MAX_TOPK
 
 
 def test_add_rmsnorm_quantize_rejections(lib):
@@ -84,3 +85,44 @@ def test_binding_refuses_before_the_library(lib):
         fp8.fp8_rmsnorm_backward(x, x.float(), torch.zeros(4), g)
     with pytest.raises(ValueError):
         fp8.fp8_rmsnorm_backward(x, x, torch.zeros(4), g)
+
+
+def test_token_logprobs_rejections(lib):
+    def call(x=A16, dtype=0, rows=4, vocab=1000, ld=1000, y=A16, k=5, lp=A16, h=A16, st=A16, tl=A16, ti=A16):
+        return lib.fp8_token_logprobs(P(x), dtype, rows, vocab, ld, P(y), k, P(lp), P(h), P(st), P(tl), P(ti), S)
+
+    assert call(dtype=2) == MODE and call(dtype=-1) == MODE
+    assert call(rows=-1) == SHAPE and call(vocab=0) == SHAPE and call(ld=999) == SHAPE and call(vocab=1 << 31, ld=1 << 31) == SHAPE
+    assert call(ld=(1 << 40) + 1) == SHAPE
+    assert call(k=-1) == SHAPE and call(k=fp8.MAX_TOPK + 1) == SHAPE and call(k=6, vocab=5) == SHAPE
+    for name in ("x", "st", "y", "tl", "ti"):
+        assert call(**{name: None}) == NULL, name
+    for name in ("y", "lp", "h", "st", "tl", "ti"):
+        assert call(**{name: MIS}) == ALIGN, name
+    assert call(x=A16 + 1) == ALIGN and call(x=A16 + 2, dtype=1) == ALIGN
+    assert call(rows=0, x=None) == OK
+
+
+def test_token_logprobs_backward_rejections(lib):
+    def call(x=A16, dtype=1, rows=4, vocab=1000, ld=1000, y=A16, st=A16, g=A16, H=A16, h=A16, out=A16 + 0x10000, ldo=1000):
+        return lib.fp8_token_logprobs_backward(P(x), dtype, rows, vocab, ld, P(y), P(st), P(g), P(H), P(h), P(out), ldo, S)
+
+    assert call(dtype=7) == MODE
+    assert call(rows=-1) == SHAPE and call(vocab=0) == SHAPE and call(ld=999) == SHAPE and call(ldo=999) == SHAPE
+    assert call(ldo=1008, out=A16) == SHAPE                                 # in place with another stride
+    for name in ("x", "st", "out", "y", "H"):
+        assert call(**{name: None}) == NULL, name
+    for name in ("y", "st", "g", "H", "h"):
+        assert call(**{name: MIS}) == ALIGN, name
+    assert call(x=A16 + 2) == ALIGN and call(out=A16 + 2) == ALIGN
+    assert call(rows=0, x=None) == OK
+
+
+def test_logits_binding_refuses(lib):
+    x = torch.zeros(4, 100)
+    with pytest.raises(ValueError):                  # not on a GPU
+        fp8.fp8_token_logprobs(x)
+    with pytest.raises(TypeError):
+        fp8.fp8_token_logprobs(x.half())
+    with pytest.raises(TypeError):
+        fp8.fp8_token_logprobs(x[0])

@@ -21,6 +21,8 @@ MAX_CONTRACTION_FPROP = 32768
 GEMM_SPLIT_MIN_WORK_DEFAULT = 160      # FP8_GEMM_SPLIT_MIN_WORK_DEFAULT
 MAX_NORM_COLS = 16384                  # FP8_MAX_NORM_COLS
 MAX_TOPK = 32                          # FP8_MAX_TOPK
+# The coefficients (a, b, c) of the steps published with the Muon optimiser.
+NEWTON_SCHULZ_COEFFICIENTS = ((3.4445, -4.7750, 2.0315),) * 5
 
 _lib = None
 
@@ -68,6 +70,8 @@ def load() -> ctypes.CDLL:
         "fp8_rmsnorm_backward_workspace_bytes": [i64, i64, p],
         "fp8_token_logprobs": [p, i32, i64, i64, i64, p, i32, p, p, p, p, p, p],
         "fp8_token_logprobs_backward": [p, i32, i64, i64, i64, p, p, p, p, p, p, i64, p],
+        "fp8_newton_schulz": [p, i32, i64, i64, i64, p, i32, ctypes.c_float, p, p, sz, p],
+        "fp8_newton_schulz_workspace_bytes": [i64, i64, i64, p],
         "fp8_selftest_silu_bf16": [p, p],
         "fp8_block_gemm_fprop": [p, p, p, p, p, i64, i64, i64, p, sz, p],
         "fp8_block_gemm_dgrad": [p, p, p, p, p, i64, i64, i64, p, sz, p],
@@ -465,6 +469,40 @@ def fp8_token_logprobs_backward(logits, targets, stats, dlogprob=None, entropy=N
                                            _stream(stream)),
            "fp8_token_logprobs_backward")
     return dlogits
+
+
+def fp8_newton_schulz_workspace_bytes(batch: int, m: int, n: int) -> int:
+    """Bytes of scratch fp8_newton_schulz needs for [batch, m, n]."""
+    k = ctypes.c_size_t(0)
+    _check(load().fp8_newton_schulz_workspace_bytes(int(batch), int(m), int(n), ctypes.byref(k)),
+           "fp8_newton_schulz_workspace_bytes")
+    return int(k.value)
+
+
+def fp8_newton_schulz(g, coefficients=NEWTON_SCHULZ_COEFFICIENTS, eps=1e-7, out=None, workspace=None, stream=None):
+    """Newton-Schulz orthogonalisation of each matrix of g ([m, n] or
+    [batch, m, n], bf16 or float32), one step per (a, b, c) of coefficients.
+    Returns a bf16 tensor of g's shape.  workspace: optional uint8 scratch of
+    fp8_newton_schulz_workspace_bytes (allocated when left out)."""
+    lib = load()
+    if g.dim() not in (2, 3) or g.dtype not in _DTYPES:
+        raise TypeError("g must be a 2-D or 3-D bfloat16 or float32 tensor")
+    _want(g, g.dtype, g.shape, "g")
+    batch, m, n = g.shape if g.dim() == 3 else (1, *g.shape)
+    steps = len(coefficients)
+    if any(len(step) != 3 for step in coefficients):
+        raise ValueError("each step takes three coefficients")
+    table = (ctypes.c_float * (3 * steps))(*[float(v) for step in coefficients for v in step])
+    new = []
+    out = _given(out, torch.bfloat16, tuple(g.shape), g, new, "out")
+    _launch_checks([("g", g), ("out", out), ("workspace", workspace)], stream)
+    if workspace is None:
+        workspace = _alloc((fp8_newton_schulz_workspace_bytes(batch, m, n),), torch.uint8, g, new)
+    _record(stream, new)
+    _check(lib.fp8_newton_schulz(_ptr(g), _DTYPES[g.dtype], batch, m, n, ctypes.cast(table, ctypes.c_void_p), steps,
+                                 float(eps), _ptr(out), *_workspace(workspace), _stream(stream)),
+           "fp8_newton_schulz")
+    return out
 
 
 def fp8_quantize_weight_128x128(w, wq=None, sw=None, wqT=None, transposed=True, stream=None):

@@ -14,6 +14,7 @@
 #include "addnorm.cuh"
 #include "gemm.cuh"
 #include "logprobs.cuh"
+#include "newton_schulz.cuh"
 #include "quantize.cuh"
 
 static_assert(fp8blk::kErrTimeout == static_cast<unsigned int>(FP8_ERR_TIMEOUT),
@@ -517,6 +518,105 @@ fp8_status launch_logp_bwd(const void* logits, int64_t rows, int64_t vocab, int6
     return last_launch_status("token log probabilities gradient launch");
 }
 
+// Newton-Schulz: the workspace's parts, each at a multiple of 256 bytes.
+struct NsLayout {
+    int64_t s, l;               // shorter and longer side
+    int64_t x_ld, s_ld;         // row strides of X and of S, Q (multiples of 64)
+    bool tall;                  // more rows than columns
+    size_t partial, x0, x1, gram, poly, bytes;
+};
+NsLayout ns_layout(int64_t batch, int64_t m, int64_t n) {
+    NsLayout w;
+    w.tall = m > n;
+    w.s = w.tall ? n : m;
+    w.l = w.tall ? m : n;
+    w.x_ld = (n + 63) / 64 * 64;
+    w.s_ld = (w.s + 63) / 64 * 64;
+    auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+    const size_t x = up(static_cast<size_t>(batch * m * w.x_ld) * 2), q = up(static_cast<size_t>(batch * w.s * w.s_ld) * 2);
+    w.partial = 0;
+    w.x0 = up(static_cast<size_t>(batch) * ns::kNormBlocks * sizeof(double));
+    w.x1 = w.x0 + x;
+    w.gram = w.x1 + x;
+    w.poly = w.gram + q;
+    w.bytes = w.poly + q;
+    return w;
+}
+
+// [batch][rows][cols] 16-bit row-major matrices with rows of ld elements.
+fp8_status make_map_3d(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t batch, int64_t ld,
+                       uint32_t box_x, uint32_t box_y, CUtensorMapSwizzle swizzle) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return FP8_ERR_CUDA;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(batch)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld) * rows * 2};
+    cuuint32_t box[3] = {box_x, box_y, 1u};
+    cuuint32_t estride[3] = {1u, 1u, 1u};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, box, estride,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        snprintf(g_detail, sizeof g_detail, "cuTensorMapEncodeTiled(3-D): CUresult %d", static_cast<int>(r));
+        return FP8_ERR_CUDA;
+    }
+    return FP8_OK;
+}
+
+std::atomic<int> g_ns_attr_done[kMaxDevices];
+std::atomic<int> g_ns_pairs[kMaxDevices][8];     // co-resident CTA pairs per kernel variant
+
+template <int MODE, bool A_MN, bool B_MN>
+fp8_status launch_ns_gemm(int dev, int sms, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
+                          const CUtensorMap& t, const ns::Params& p, cudaStream_t s) {
+    constexpr int variant = MODE * 2 + (MODE == ns::kGram ? A_MN : B_MN);
+    auto kernel = ns::gemm_kernel<MODE, A_MN, B_MN>;
+    if ((g_ns_attr_done[dev].load(std::memory_order_acquire) & (1 << variant)) == 0) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, ns::SMEM_BYTES);
+        if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute(newton-schulz)", e);
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(sms & ~1), 1, 1);
+        cfg.blockDim = dim3(ns::THREADS, 1, 1);
+        cfg.dynamicSmemBytes = ns::SMEM_BYTES;
+        int pairs = 0;
+        e = cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg);
+        if (e != cudaSuccess) return cuda_fail("cudaOccupancyMaxActiveClusters(newton-schulz)", e);
+        if (pairs <= 0) return cuda_fail("newton-schulz kernel cannot be resident", cudaErrorInvalidConfiguration);
+        g_ns_pairs[dev][variant].store(pairs, std::memory_order_relaxed);
+        g_ns_attr_done[dev].fetch_or(1 << variant, std::memory_order_release);
+    }
+    const int64_t total = static_cast<int64_t>(p.tiles) * p.batch;
+    const int pairs = g_ns_pairs[dev][variant].load(std::memory_order_relaxed);
+    const unsigned grid = 2u * static_cast<unsigned>(total < pairs ? total : pairs);
+    const cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(ns::THREADS), ns::SMEM_BYTES, s, a, b, c, t, p);
+    if (e != cudaSuccess) return cuda_fail("newton-schulz product launch", e);
+    return last_launch_status("newton-schulz product launch");
+}
+
+template <typename T>
+fp8_status launch_ns_cast(const T* g, int64_t batch, int64_t m, int64_t n, int64_t ld, double* partial, float eps,
+                          float scale, __half* x, int sms, cudaStream_t s) {
+    const bool vec = n * static_cast<int64_t>(sizeof(T)) % 16 == 0 && aligned16(g) && n % 8 == 0;
+    const int64_t per_block = static_cast<int64_t>(ns::kNormThreads) * 16;
+    int64_t parts = (m * n + per_block - 1) / per_block;
+    const int64_t want = (8 * static_cast<int64_t>(sms) + batch - 1) / batch;
+    if (parts > want) parts = want;
+    if (parts > ns::kNormBlocks) parts = ns::kNormBlocks;
+    const dim3 block(ns::kNormThreads);
+    cudaError_t e;
+    auto norm = vec ? ns::norm_kernel<T, true> : ns::norm_kernel<T, false>;
+    e = launch_pdl(norm, dim3(static_cast<unsigned>(parts), static_cast<unsigned>(batch)), block, 0, s, g, m * n, partial);
+    if (e != cudaSuccess) return cuda_fail("newton-schulz norm launch", e);
+    int64_t blocks = (m * (ld / 8) + ns::kNormThreads - 1) / ns::kNormThreads;
+    const int64_t cap = (16 * static_cast<int64_t>(sms) + batch - 1) / batch;
+    if (blocks > cap) blocks = cap;
+    auto cast = vec ? ns::cast_kernel<T, true> : ns::cast_kernel<T, false>;
+    e = launch_pdl(cast, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(batch)), block, 0, s, g,
+                   static_cast<int>(m), static_cast<int>(n), static_cast<int>(ld), static_cast<const double*>(partial),
+                   static_cast<int>(parts), eps, scale, x);
+    if (e != cudaSuccess) return cuda_fail("newton-schulz cast launch", e);
+    return last_launch_status("newton-schulz cast launch");
+}
+
 // Scratch of fp8_block_gemm_wgrad_static_ws: the split schedule's workspace
 // as a file-scope device array, for callers that cannot allocate device
 // memory.  Every GPU that loads the library holds it until the process
@@ -777,6 +877,111 @@ fp8_status fp8_token_logprobs_backward(const void* logits, int dtype, int64_t ro
                                               dlogits, ld_out, s);
     return launch_logp_bwd<float>(logits, rows, vocab, ld, targets, stats, dlogprob, entropy, dentropy, dlogits,
                                   ld_out, s);
+}
+
+fp8_status fp8_newton_schulz_workspace_bytes(int64_t batch, int64_t m, int64_t n, size_t* bytes) {
+    if (!bytes) return FP8_ERR_NULL;
+    if (batch < 0 || m < 1 || n < 1 || batch > FP8_NS_MAX_BATCH || m > ns::kMaxSide || n > ns::kMaxSide)
+        return FP8_ERR_SHAPE;
+    *bytes = batch ? ns_layout(batch, m, n).bytes : 0;
+    return FP8_OK;
+}
+
+fp8_status fp8_newton_schulz(const void* g, int dtype, int64_t batch, int64_t m, int64_t n, const float* coefficients,
+                             int steps, float eps, void* out_bf16, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+    if (!dtype_ok(dtype)) return FP8_ERR_MODE;
+    if (batch < 0 || m < 1 || n < 1 || batch > FP8_NS_MAX_BATCH || m > ns::kMaxSide || n > ns::kMaxSide)
+        return FP8_ERR_SHAPE;
+    if (steps < 1 || steps > FP8_NS_MAX_STEPS || !(eps >= 0.0f) || eps > 3.0e38f) return FP8_ERR_SHAPE;
+    if (!coefficients) return FP8_ERR_NULL;
+    for (int i = 0; i < 3 * steps; ++i)
+        if (!(coefficients[i] >= -FP8_NS_MAX_COEFFICIENT && coefficients[i] <= FP8_NS_MAX_COEFFICIENT)) return FP8_ERR_SHAPE;
+    if (batch == 0) return FP8_OK;
+    if (!g || !out_bf16 || !workspace) return FP8_ERR_NULL;
+    if (!aligned16(g) || !aligned16(out_bf16) || !aligned16(workspace)) return FP8_ERR_ALIGN;
+    const NsLayout w = ns_layout(batch, m, n);
+    if (workspace_bytes < w.bytes) return FP8_ERR_SHAPE;
+    int dev = 0, sms = 0;
+    fp8_status st = current_device(&dev);
+    if (st != FP8_OK) return st;
+    if ((st = sm_count(dev, &sms)) != FP8_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    __half* x[2] = {reinterpret_cast<__half*>(ws + w.x0), reinterpret_cast<__half*>(ws + w.x1)};
+    __half* gram = reinterpret_cast<__half*>(ws + w.gram);
+    __half* poly = reinterpret_cast<__half*>(ws + w.poly);
+
+    // the first X times the power of two at or below sqrt(m n)
+    float scale = 1.0f;
+    while (4.0 * scale * scale <= static_cast<double>(m) * static_cast<double>(n)) scale *= 2.0f;
+    double* partial = reinterpret_cast<double*>(ws + w.partial);
+    st = dtype == FP8_F32 ? launch_ns_cast(static_cast<const float*>(g), batch, m, n, w.x_ld, partial, eps, scale, x[0], sms, s)
+                          : launch_ns_cast(static_cast<const __nv_bfloat16*>(g), batch, m, n, w.x_ld, partial, eps, scale,
+                                           x[0], sms, s);
+    if (st != FP8_OK) return st;
+
+    constexpr CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B, flat = CU_TENSOR_MAP_SWIZZLE_NONE;
+    CUtensorMap x_rows[2], x_cols[2], x_out[2], s_in, s_out, s_outT, q_in, q_out, q_outT, final_map;
+    for (int i = 0; i < 2; ++i) {
+        if ((st = make_map_3d(&x_rows[i], x[i], w.x_ld, m, batch, w.x_ld, 64, 128, sw)) != FP8_OK) return st;
+        if ((st = make_map_3d(&x_cols[i], x[i], w.x_ld, m, batch, w.x_ld, 64, 64, sw)) != FP8_OK) return st;
+        if ((st = make_map_3d(&x_out[i], x[i], w.x_ld, m, batch, w.x_ld, 64, 32, sw)) != FP8_OK) return st;
+    }
+    if ((st = make_map_3d(&s_in, gram, w.s_ld, w.s, batch, w.s_ld, 64, 128, sw)) != FP8_OK) return st;
+    if ((st = make_map_3d(&s_out, gram, w.s_ld, w.s, batch, w.s_ld, 64, 32, sw)) != FP8_OK) return st;
+    if ((st = make_map_3d(&s_outT, gram, w.s_ld, w.s, batch, w.s_ld, 32, 64, flat)) != FP8_OK) return st;
+    if ((st = make_map_3d(&q_in, poly, w.s_ld, w.s, batch, w.s_ld, 64, 128, sw)) != FP8_OK) return st;
+    if ((st = make_map_3d(&q_out, poly, w.s_ld, w.s, batch, w.s_ld, 64, 32, sw)) != FP8_OK) return st;
+    if ((st = make_map_3d(&q_outT, poly, w.s_ld, w.s, batch, w.s_ld, 32, 64, flat)) != FP8_OK) return st;
+    const bool tma_out = n % 8 == 0;             // the output's rows are multiples of 16 bytes
+    if (tma_out) {
+        if ((st = make_map_3d(&final_map, out_bf16, n, m, batch, n, 64, 32, sw)) != FP8_OK) return st;
+    } else {
+        final_map = x_out[0];                    // not used
+    }
+
+    ns::Params base{};
+    base.batch = static_cast<int>(batch);
+    base.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+    const int side = static_cast<int>((w.s + 255) / 256);
+    for (int i = 0; i < steps; ++i) {
+        const int cur = i & 1;
+        const float in = i == 0 ? 1.0f / scale : 1.0f;       // what X has to be multiplied by
+        ns::Params p = base;                                 // S
+        p.M = p.N = static_cast<int>(w.s);
+        p.K = static_cast<int>(w.l);
+        p.tiles_m = p.tiles_n = side;
+        p.tiles = side * (side + 1) / 2;
+        p.alpha = in * in;
+        st = w.tall ? launch_ns_gemm<ns::kGram, true, true>(dev, sms, x_cols[cur], x_cols[cur], s_out, s_outT, p, s)
+                    : launch_ns_gemm<ns::kGram, false, false>(dev, sms, x_rows[cur], x_rows[cur], s_out, s_outT, p, s);
+        if (st != FP8_OK) return st;
+        p.K = static_cast<int>(w.s);                         // Q
+        p.a = coefficients[3 * i];
+        p.b = coefficients[3 * i + 1];
+        p.c = coefficients[3 * i + 2];
+        p.s = gram;
+        p.s_ld = w.s_ld;
+        st = launch_ns_gemm<ns::kPoly, false, false>(dev, sms, s_in, s_in, q_out, q_outT, p, s);
+        if (st != FP8_OK) return st;
+        p = base;                                            // X
+        p.M = static_cast<int>(m);
+        p.N = static_cast<int>(n);
+        p.K = static_cast<int>(w.s);
+        p.tiles_m = static_cast<int>((m + 255) / 256);
+        p.tiles_n = static_cast<int>((n + 255) / 256);
+        p.tiles = p.tiles_m * p.tiles_n;
+        p.row_fast = w.tall ? 0 : 1;
+        p.alpha = in;
+        p.final_out = i == steps - 1;
+        p.out = p.final_out && !tma_out ? static_cast<__nv_bfloat16*>(out_bf16) : nullptr;
+        const CUtensorMap& c = p.final_out ? final_map : x_out[cur ^ 1];
+        st = w.tall ? launch_ns_gemm<ns::kApply, false, false>(dev, sms, x_rows[cur], q_in, c, c, p, s)
+                    : launch_ns_gemm<ns::kApply, false, true>(dev, sms, q_in, x_cols[cur], c, c, p, s);
+        if (st != FP8_OK) return st;
+    }
+    return FP8_OK;
 }
 
 fp8_status fp8_quantize_weight_128x128(const void* w_bf16, int64_t n, int64_t k, uint8_t* wq,

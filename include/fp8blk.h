@@ -275,7 +275,7 @@ fp8_status fp8_rmsnorm_backward(const void *dy_bf16, const void *s_bf16, const f
                                 void *workspace, size_t workspace_bytes, void *stream);
 fp8_status fp8_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols, size_t *bytes);
 
-/* Element types of logits and gradients. */
+/* Element types of logits and of gradients to orthogonalise. */
 enum {
     FP8_BF16 = 0,
     FP8_F32 = 1
@@ -339,6 +339,47 @@ fp8_status fp8_token_logprobs_backward(const void *logits, int dtype, int64_t ro
                                        const float *dlogprob, const float *entropy,
                                        const float *dentropy, void *dlogits, int64_t ld_out,
                                        void *stream);
+
+/* Limits of fp8_newton_schulz. */
+#define FP8_NS_MAX_BATCH 4096
+#define FP8_NS_MAX_STEPS 32
+#define FP8_NS_MAX_COEFFICIENT 64.0f
+
+/*
+ * Newton-Schulz orthogonalisation, the step the Muon optimiser takes on a
+ * weight's (main) gradient: X0 = G / (|G|_F + eps), then per step with its
+ * coefficients (a, b, c)
+ *   S = X X^T,  X <- a X + (b S + c S S) X
+ * (for more rows than columns the same on the transpose, S = X^T X), result
+ * rounded to BF16.  The norm is taken in FP64.  Products take FP16 operands
+ * (S, a I + b S + c S S and X are rounded to FP16 once per step, 2^-11) with
+ * FP32 accumulation; with the usual coefficients, whose X stays below about
+ * 1.3 in spectral norm, no value leaves FP16's range.  Coefficients that let X
+ * grow past it give infinities.  A zero matrix gives zeros; a non-finite
+ * element makes its whole matrix NaN.  Results repeat run to run.  Passage:
+ * Puro-2B-Base model card (friendli.ai), training-setup paragraph (MuonH on
+ * the matrices, FP32 optimizer state); the pages give neither the iteration
+ * nor its coefficients, so this is the published Muon iteration with the
+ * caller's coefficients.
+ *
+ *   g       [batch, m, n], dtype FP8_BF16 or FP8_F32 (for example the main
+ *           gradient fp8_block_gemm_wgrad_accum_f32 adds to).
+ *   0 <= batch <= FP8_NS_MAX_BATCH; 1 <= m, n <= 32768.
+ *   coefficients: host array [steps][3], finite and at most
+ *           FP8_NS_MAX_COEFFICIENT in magnitude; 1 <= steps <=
+ *           FP8_NS_MAX_STEPS.  Read before the call returns.
+ *   eps     >= 0, finite.
+ *   out_bf16 [batch, m, n], written; must not overlap g or the workspace.
+ *   workspace: workspace_bytes >= fp8_newton_schulz_workspace_bytes(batch, m,
+ *           n) of scratch (too small a one is FP8_ERR_SHAPE); its contents
+ *           before the call do not matter.  Two calls that may run at the
+ *           same time need different workspaces.
+ * All pointers are 16-byte aligned.  batch == 0 is a no-op.
+ */
+fp8_status fp8_newton_schulz(const void *g, int dtype, int64_t batch, int64_t m, int64_t n,
+                             const float *coefficients, int steps, float eps, void *out_bf16,
+                             void *workspace, size_t workspace_bytes, void *stream);
+fp8_status fp8_newton_schulz_workspace_bytes(int64_t batch, int64_t m, int64_t n, size_t *bytes);
 
 /*
  * Weight quantizer, 128x128 blocks.

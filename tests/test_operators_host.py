@@ -126,3 +126,37 @@ def test_logits_binding_refuses(lib):
         fp8.fp8_token_logprobs(x.half())
     with pytest.raises(TypeError):
         fp8.fp8_token_logprobs(x[0])
+
+
+def test_newton_schulz_rejections(lib):
+    def call(g=A16, dtype=1, batch=1, m=64, n=64, coeff=(1.0, 2.0, 3.0), steps=1, eps=0.0, out=A16, ws=A16, size=1 << 40):
+        table = (ctypes.c_float * max(1, len(coeff)))(*coeff) if coeff is not None else None
+        c = ctypes.cast(table, ctypes.c_void_p) if table is not None else None
+        return lib.fp8_newton_schulz(P(g), dtype, batch, m, n, c, steps, eps, P(out), P(ws), size, S)
+
+    assert call(dtype=2) == MODE
+    assert call(batch=-1) == SHAPE and call(m=0) == SHAPE and call(n=0) == SHAPE and call(m=32769) == SHAPE
+    assert call(batch=4097) == SHAPE and call(steps=0) == SHAPE and call(steps=33) == SHAPE
+    assert call(eps=-1.0) == SHAPE and call(eps=float("nan")) == SHAPE
+    assert call(coeff=(1.0, float("nan"), 0.0)) == SHAPE and call(coeff=(1.0, 65.0, 0.0)) == SHAPE
+    assert call(coeff=None) == NULL
+    for name in ("g", "out", "ws"):
+        assert call(**{name: None}) == NULL and call(**{name: MIS}) == ALIGN, name
+    assert call(size=1024) == SHAPE
+    assert call(batch=0, g=None) == OK
+    n = ctypes.c_size_t(7)
+    assert lib.fp8_newton_schulz_workspace_bytes(1, 64, 64, None) == NULL
+    assert lib.fp8_newton_schulz_workspace_bytes(1, 0, 64, ctypes.byref(n)) == SHAPE
+    assert lib.fp8_newton_schulz_workspace_bytes(0, 64, 64, ctypes.byref(n)) == OK and n.value == 0
+    assert lib.fp8_newton_schulz_workspace_bytes(2, 100, 130, ctypes.byref(n)) == OK
+    assert n.value >= 2 * (2 * 100 * 192 + 2 * 100 * 128) * 2
+
+
+def test_newton_schulz_binding_refuses(lib):
+    g = torch.zeros(8, 8)
+    with pytest.raises(ValueError):                  # not on a GPU
+        fp8.fp8_newton_schulz(g)
+    with pytest.raises(TypeError):
+        fp8.fp8_newton_schulz(g.half())
+    with pytest.raises(TypeError):
+        fp8.fp8_newton_schulz(g[0])

@@ -523,7 +523,7 @@ struct NsLayout {
     int64_t s, l;               // shorter and longer side
     int64_t x_ld, s_ld;         // row strides of X and of S, Q (multiples of 64)
     bool tall;                  // more rows than columns
-    size_t partial, x0, x1, gram, poly, bytes;
+    size_t partial, x[2], lo[2], gram, poly, bytes;   // X and what FP16 leaves of it, twice
 };
 NsLayout ns_layout(int64_t batch, int64_t m, int64_t n) {
     NsLayout w;
@@ -535,9 +535,11 @@ NsLayout ns_layout(int64_t batch, int64_t m, int64_t n) {
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     const size_t x = up(static_cast<size_t>(batch * m * w.x_ld) * 2), q = up(static_cast<size_t>(batch * w.s * w.s_ld) * 2);
     w.partial = 0;
-    w.x0 = up(static_cast<size_t>(batch) * ns::kNormBlocks * sizeof(double));
-    w.x1 = w.x0 + x;
-    w.gram = w.x1 + x;
+    w.x[0] = up(static_cast<size_t>(batch) * ns::kNormBlocks * sizeof(double));
+    w.x[1] = w.x[0] + x;
+    w.lo[0] = w.x[1] + x;
+    w.lo[1] = w.lo[0] + x;
+    w.gram = w.lo[1] + x;
     w.poly = w.gram + q;
     w.bytes = w.poly + q;
     return w;
@@ -567,7 +569,7 @@ std::atomic<int> g_ns_pairs[kMaxDevices][8];     // co-resident CTA pairs per ke
 
 template <int MODE, bool A_MN, bool B_MN>
 fp8_status launch_ns_gemm(int dev, int sms, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
-                          const CUtensorMap& t, const ns::Params& p, cudaStream_t s) {
+                          const CUtensorMap& t, ns::Params p, int64_t batch, cudaStream_t s) {
     constexpr int variant = MODE * 2 + (MODE == ns::kGram ? A_MN : B_MN);
     auto kernel = ns::gemm_kernel<MODE, A_MN, B_MN>;
     if ((g_ns_attr_done[dev].load(std::memory_order_acquire) & (1 << variant)) == 0) {
@@ -584,9 +586,15 @@ fp8_status launch_ns_gemm(int dev, int sms, const CUtensorMap& a, const CUtensor
         g_ns_pairs[dev][variant].store(pairs, std::memory_order_relaxed);
         g_ns_attr_done[dev].fetch_or(1 << variant, std::memory_order_release);
     }
-    const int64_t total = static_cast<int64_t>(p.tiles) * p.batch;
+    const int64_t total = static_cast<int64_t>(p.tiles) * batch;
     const int pairs = g_ns_pairs[dev][variant].load(std::memory_order_relaxed);
-    const unsigned grid = 2u * static_cast<unsigned>(total < pairs ? total : pairs);
+    // Whole tiles for the full waves; the rest in halves when one wave of
+    // pairs can take all of them (a half tile takes about 3/4 of a whole one's
+    // time: its operands' traffic shrinks less than its products).
+    const int64_t rest = total % pairs;
+    p.full = static_cast<int>(2 * rest <= pairs ? total - rest : total);
+    p.units = static_cast<int>(p.full + 2 * (total - p.full));
+    const unsigned grid = 2u * static_cast<unsigned>(p.units < pairs ? p.units : pairs);
     const cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(ns::THREADS), ns::SMEM_BYTES, s, a, b, c, t, p);
     if (e != cudaSuccess) return cuda_fail("newton-schulz product launch", e);
     return last_launch_status("newton-schulz product launch");
@@ -594,7 +602,7 @@ fp8_status launch_ns_gemm(int dev, int sms, const CUtensorMap& a, const CUtensor
 
 template <typename T>
 fp8_status launch_ns_cast(const T* g, int64_t batch, int64_t m, int64_t n, int64_t ld, double* partial, float eps,
-                          float scale, __half* x, int sms, cudaStream_t s) {
+                          float scale, __half* hi, __half* lo, int sms, cudaStream_t s) {
     const bool vec = n * static_cast<int64_t>(sizeof(T)) % 16 == 0 && aligned16(g) && n % 8 == 0;
     const int64_t per_block = static_cast<int64_t>(ns::kNormThreads) * 16;
     int64_t parts = (m * n + per_block - 1) / per_block;
@@ -612,7 +620,7 @@ fp8_status launch_ns_cast(const T* g, int64_t batch, int64_t m, int64_t n, int64
     auto cast = vec ? ns::cast_kernel<T, true> : ns::cast_kernel<T, false>;
     e = launch_pdl(cast, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(batch)), block, 0, s, g,
                    static_cast<int>(m), static_cast<int>(n), static_cast<int>(ld), static_cast<const double*>(partial),
-                   static_cast<int>(parts), eps, scale, x);
+                   static_cast<int>(parts), eps, scale, hi, lo);
     if (e != cudaSuccess) return cuda_fail("newton-schulz cast launch", e);
     return last_launch_status("newton-schulz cast launch");
 }
@@ -908,30 +916,40 @@ fp8_status fp8_newton_schulz(const void* g, int dtype, int64_t batch, int64_t m,
     if ((st = sm_count(dev, &sms)) != FP8_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    __half* x[2] = {reinterpret_cast<__half*>(ws + w.x0), reinterpret_cast<__half*>(ws + w.x1)};
+    __half *x[2], *lo[2];
+    for (int i = 0; i < 2; ++i) {
+        x[i] = reinterpret_cast<__half*>(ws + w.x[i]);
+        lo[i] = reinterpret_cast<__half*>(ws + w.lo[i]);
+    }
     __half* gram = reinterpret_cast<__half*>(ws + w.gram);
     __half* poly = reinterpret_cast<__half*>(ws + w.poly);
 
-    // the first X times the power of two at or below sqrt(m n)
+    // X is kept times the power of two at or below sqrt(m n), at most 2^13
+    // (entries of X up to 8 then stay inside FP16's range).
     float scale = 1.0f;
-    while (4.0 * scale * scale <= static_cast<double>(m) * static_cast<double>(n)) scale *= 2.0f;
+    while (scale < 8192.0f && 4.0 * scale * scale <= static_cast<double>(m) * static_cast<double>(n)) scale *= 2.0f;
     double* partial = reinterpret_cast<double*>(ws + w.partial);
-    st = dtype == FP8_F32 ? launch_ns_cast(static_cast<const float*>(g), batch, m, n, w.x_ld, partial, eps, scale, x[0], sms, s)
+    st = dtype == FP8_F32 ? launch_ns_cast(static_cast<const float*>(g), batch, m, n, w.x_ld, partial, eps, scale, x[0],
+                                           lo[0], sms, s)
                           : launch_ns_cast(static_cast<const __nv_bfloat16*>(g), batch, m, n, w.x_ld, partial, eps, scale,
-                                           x[0], sms, s);
+                                           x[0], lo[0], sms, s);
     if (st != FP8_OK) return st;
 
     constexpr CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B, flat = CU_TENSOR_MAP_SWIZZLE_NONE;
-    CUtensorMap x_rows[2], x_cols[2], x_out[2], s_in, s_out, s_outT, q_in, q_out, q_outT, final_map;
+    CUtensorMap x_rows[2], x_half[2], x_out[2], lo_out[2], s_in, s_half, s_out, s_outT, q_in, q_half, q_out, q_outT,
+        final_map;
     for (int i = 0; i < 2; ++i) {
         if ((st = make_map_3d(&x_rows[i], x[i], w.x_ld, m, batch, w.x_ld, 64, 128, sw)) != FP8_OK) return st;
-        if ((st = make_map_3d(&x_cols[i], x[i], w.x_ld, m, batch, w.x_ld, 64, 64, sw)) != FP8_OK) return st;
+        if ((st = make_map_3d(&x_half[i], x[i], w.x_ld, m, batch, w.x_ld, 64, 64, sw)) != FP8_OK) return st;
+        if ((st = make_map_3d(&lo_out[i], lo[i], w.x_ld, m, batch, w.x_ld, 64, 32, sw)) != FP8_OK) return st;
         if ((st = make_map_3d(&x_out[i], x[i], w.x_ld, m, batch, w.x_ld, 64, 32, sw)) != FP8_OK) return st;
     }
     if ((st = make_map_3d(&s_in, gram, w.s_ld, w.s, batch, w.s_ld, 64, 128, sw)) != FP8_OK) return st;
+    if ((st = make_map_3d(&s_half, gram, w.s_ld, w.s, batch, w.s_ld, 64, 64, sw)) != FP8_OK) return st;
     if ((st = make_map_3d(&s_out, gram, w.s_ld, w.s, batch, w.s_ld, 64, 32, sw)) != FP8_OK) return st;
     if ((st = make_map_3d(&s_outT, gram, w.s_ld, w.s, batch, w.s_ld, 32, 64, flat)) != FP8_OK) return st;
     if ((st = make_map_3d(&q_in, poly, w.s_ld, w.s, batch, w.s_ld, 64, 128, sw)) != FP8_OK) return st;
+    if ((st = make_map_3d(&q_half, poly, w.s_ld, w.s, batch, w.s_ld, 64, 64, sw)) != FP8_OK) return st;
     if ((st = make_map_3d(&q_out, poly, w.s_ld, w.s, batch, w.s_ld, 64, 32, sw)) != FP8_OK) return st;
     if ((st = make_map_3d(&q_outT, poly, w.s_ld, w.s, batch, w.s_ld, 32, 64, flat)) != FP8_OK) return st;
     const bool tma_out = n % 8 == 0;             // the output's rows are multiples of 16 bytes
@@ -942,28 +960,27 @@ fp8_status fp8_newton_schulz(const void* g, int dtype, int64_t batch, int64_t m,
     }
 
     ns::Params base{};
-    base.batch = static_cast<int>(batch);
     base.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
     const int side = static_cast<int>((w.s + 255) / 256);
     for (int i = 0; i < steps; ++i) {
         const int cur = i & 1;
-        const float in = i == 0 ? 1.0f / scale : 1.0f;       // what X has to be multiplied by
+        const bool lin = i <= ns::kCarry;                    // X's linear term from both its parts
         ns::Params p = base;                                 // S
         p.M = p.N = static_cast<int>(w.s);
         p.K = static_cast<int>(w.l);
         p.tiles_m = p.tiles_n = side;
         p.tiles = side * (side + 1) / 2;
-        p.alpha = in * in;
-        st = w.tall ? launch_ns_gemm<ns::kGram, true, true>(dev, sms, x_cols[cur], x_cols[cur], s_out, s_outT, p, s)
-                    : launch_ns_gemm<ns::kGram, false, false>(dev, sms, x_rows[cur], x_rows[cur], s_out, s_outT, p, s);
+        p.alpha = 1.0f / (scale * scale);
+        st = w.tall ? launch_ns_gemm<ns::kGram, true, true>(dev, sms, x_half[cur], x_half[cur], s_out, s_outT, p, batch, s)
+                    : launch_ns_gemm<ns::kGram, false, false>(dev, sms, x_rows[cur], x_half[cur], s_out, s_outT, p, batch, s);
         if (st != FP8_OK) return st;
         p.K = static_cast<int>(w.s);                         // Q
-        p.a = coefficients[3 * i];
+        p.a = lin ? 0.0f : coefficients[3 * i];
         p.b = coefficients[3 * i + 1];
         p.c = coefficients[3 * i + 2];
-        p.s = gram;
-        p.s_ld = w.s_ld;
-        st = launch_ns_gemm<ns::kPoly, false, false>(dev, sms, s_in, s_in, q_out, q_outT, p, s);
+        p.e0 = gram;
+        p.e_ld = w.s_ld;
+        st = launch_ns_gemm<ns::kPoly, false, false>(dev, sms, s_in, s_half, q_out, q_outT, p, batch, s);
         if (st != FP8_OK) return st;
         p = base;                                            // X
         p.M = static_cast<int>(m);
@@ -973,12 +990,19 @@ fp8_status fp8_newton_schulz(const void* g, int dtype, int64_t batch, int64_t m,
         p.tiles_n = static_cast<int>((n + 255) / 256);
         p.tiles = p.tiles_m * p.tiles_n;
         p.row_fast = w.tall ? 0 : 1;
-        p.alpha = in;
+        p.alpha = 1.0f / scale;
         p.final_out = i == steps - 1;
+        if (lin) {
+            p.a = coefficients[3 * i];
+            p.e0 = x[cur];
+            p.e1 = lo[cur];
+            p.e_ld = w.x_ld;
+        }
+        p.carry = i < ns::kCarry && !p.final_out;
         p.out = p.final_out && !tma_out ? static_cast<__nv_bfloat16*>(out_bf16) : nullptr;
         const CUtensorMap& c = p.final_out ? final_map : x_out[cur ^ 1];
-        st = w.tall ? launch_ns_gemm<ns::kApply, false, false>(dev, sms, x_rows[cur], q_in, c, c, p, s)
-                    : launch_ns_gemm<ns::kApply, false, true>(dev, sms, q_in, x_cols[cur], c, c, p, s);
+        st = w.tall ? launch_ns_gemm<ns::kApply, false, false>(dev, sms, x_rows[cur], q_half, c, lo_out[cur ^ 1], p, batch, s)
+                    : launch_ns_gemm<ns::kApply, false, true>(dev, sms, q_in, x_half[cur], c, lo_out[cur ^ 1], p, batch, s);
         if (st != FP8_OK) return st;
     }
     return FP8_OK;

@@ -352,10 +352,11 @@ fp8_status fp8_token_logprobs_backward(const void *logits, int dtype, int64_t ro
  *   S = X X^T,  X <- a X + (b S + c S S) X
  * (for more rows than columns the same on the transpose, S = X^T X), result
  * rounded to BF16.  The norm is taken in FP64.  Products take FP16 operands
- * (S, a I + b S + c S S and X are rounded to FP16 once per step, 2^-11) with
- * FP32 accumulation; with the usual coefficients, whose X stays below about
- * 1.3 in spectral norm, no value leaves FP16's range.  Coefficients that let X
- * grow past it give infinities.  A zero matrix gives zeros; a non-finite
+ * (S, its polynomial and X are rounded to FP16 once per step, 2^-11; the first
+ * two steps carry X in two FP16 parts) with FP32 accumulation; with the usual
+ * coefficients, whose X stays below about 1.3 in spectral norm, no value
+ * leaves FP16's range.  Coefficients that let entries of X grow past 4 give
+ * infinities.  A zero matrix gives zeros; a non-finite
  * element makes its whole matrix NaN.  Results repeat run to run.  Passage:
  * Puro-2B-Base model card (friendli.ai), training-setup paragraph (MuonH on
  * the matrices, FP32 optimizer state); the pages give neither the iteration

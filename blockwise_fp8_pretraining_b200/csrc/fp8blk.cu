@@ -474,10 +474,13 @@ bool element_aligned(const void* p, int dtype) {
     return (reinterpret_cast<uintptr_t>(p) & (dtype == FP8_BF16 ? 1u : 3u)) == 0;
 }
 
-// A row of logits over `ranks` CTAs of `threads` threads: rows are split until
-// the GPU's SMs have several CTAs each (their reductions then hide behind
-// others' loads) as long as every CTA still has 16 KB of the row; a thread has
-// at least one batch of 16-byte vectors.
+// A row of logits over `ranks` CTAs.  Few rows are split as long as every CTA
+// can be resident at once and has 16 KB of the row.  An SM holds 1024 threads:
+// blocks are made small enough for all rows to be resident together where that
+// is possible (a second, mostly empty wave would double the time), and large
+// where there are many waves anyway (fewer rows at once, less left over at the
+// end).  A thread has at least one batch of 16-byte vectors; rows of one warp
+// share a block.
 template <typename T>
 fp8_status launch_logp(const void* logits, int64_t rows, int64_t vocab, int64_t ld, const int64_t* targets, int topk,
                        float* logprob, float* entropy, float* stats, float* top_logprob, int64_t* top_index,
@@ -488,15 +491,22 @@ fp8_status launch_logp(const void* logits, int64_t rows, int64_t vocab, int64_t 
     if ((st = sm_count(dev, &sms)) != FP8_OK) return st;
     const int64_t bytes = vocab * static_cast<int64_t>(sizeof(T));
     int ranks = 1;
-    while (ranks < logp::kMaxRanks && rows * ranks < 8 * static_cast<int64_t>(sms) && bytes / (2 * ranks) >= 16384)
-        ranks *= 2;
-    const int threads = pow2_between(bytes / ranks / (16 * logp::kBatch), 32, logp::kMaxThreads);
-    if (rows > kMaxDim / ranks) return FP8_ERR_SHAPE;
+    while (ranks < logp::kMaxRanks && rows * ranks <= sms && bytes / (2 * ranks) >= 16384) ranks *= 2;
+    const int64_t ctas = rows * ranks;
+    const int most = ctas <= 2 * sms || ctas > 8 * sms ? logp::kMaxThreads : ctas <= 4 * sms ? 256 : 128;
+    const int threads = pow2_between(bytes / ranks / (16 * logp::kBatch), 32, most);
+    const int warps = threads / 32, teams = warps == 1 ? logp::kTeams : 1;
+    const int64_t grid = (ctas + teams - 1) / teams;
+    if (grid > kMaxDim) return FP8_ERR_SHAPE;
     auto kernel = topk ? logp::forward_kernel<T, true> : logp::forward_kernel<T, false>;
-    const cudaError_t e = launch_pdl_cluster(
-        kernel, dim3(static_cast<unsigned>(rows * ranks)), dim3(static_cast<unsigned>(threads)),
-        static_cast<unsigned>(ranks), s, static_cast<const T*>(logits), vocab, ld, targets, topk, ranks, logprob,
-        entropy, reinterpret_cast<float2*>(stats), top_logprob, top_index);
+    const T* x = static_cast<const T*>(logits);
+    float2* st2 = reinterpret_cast<float2*>(stats);
+    const dim3 blocks(static_cast<unsigned>(grid)), block(static_cast<unsigned>(threads * teams));
+    const cudaError_t e =
+        ranks > 1 ? launch_pdl_cluster(kernel, blocks, block, static_cast<unsigned>(ranks), s, x, rows, vocab, ld,
+                                       targets, topk, ranks, warps, logprob, entropy, st2, top_logprob, top_index)
+                  : launch_pdl(kernel, blocks, block, 0, s, x, rows, vocab, ld, targets, topk, ranks, warps, logprob,
+                               entropy, st2, top_logprob, top_index);
     if (e != cudaSuccess) return cuda_fail("token log probabilities launch", e);
     return last_launch_status("token log probabilities launch");
 }
@@ -510,9 +520,10 @@ fp8_status launch_logp_bwd(const void* logits, int64_t rows, int64_t vocab, int6
     const int64_t per = static_cast<int64_t>(threads) * logp::kBatch;
     const int64_t chunks = nvec > per ? (nvec + per - 1) / per : 1;
     if (rows > kMaxDim / chunks) return FP8_ERR_SHAPE;
-    const cudaError_t e = launch_pdl(logp::backward_kernel<T>, dim3(static_cast<unsigned>(rows * chunks)),
-                                     dim3(static_cast<unsigned>(threads)), 0, s, static_cast<const T*>(logits), vocab,
-                                     ld, targets, reinterpret_cast<const float2*>(stats), dlogprob, entropy, dentropy,
+    auto kernel = dentropy ? logp::backward_kernel<T, true> : logp::backward_kernel<T, false>;
+    const cudaError_t e = launch_pdl(kernel, dim3(static_cast<unsigned>(rows * chunks)),
+                                     dim3(static_cast<unsigned>(threads)), 0, s, static_cast<const T*>(logits), vocab, ld,
+                                     targets, reinterpret_cast<const float2*>(stats), dlogprob, entropy, dentropy,
                                      chunks, static_cast<T*>(dlogits), ld_out);
     if (e != cudaSuccess) return cuda_fail("token log probabilities gradient launch", e);
     return last_launch_status("token log probabilities gradient launch");

@@ -114,12 +114,12 @@ def _check(status: int, where: str):
         raise Fp8Error(status, where)
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+def _stream(stream) -> int:
+    if stream is None:                 # the handle alone: a torch Stream object costs a microsecond
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _check_devices(named, current: int, stream=None) -> None:
@@ -149,11 +149,13 @@ def _record(stream, allocated) -> None:
                 t.record_stream(stream)
 
 
-def _ptr(t: torch.Tensor | None) -> ctypes.c_void_p:
-    return ctypes.c_void_p(0 if t is None else t.data_ptr())
+def _ptr(t: torch.Tensor | None) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def _want(t: torch.Tensor, dtype, shape, name):
+    if t.is_cuda and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+        return t
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -292,7 +294,11 @@ def fp8_rmsnorm_quantize_1x128(x, rstd, gamma, mode=BOTH, q_row=None, s_row=None
 
 
 def _alloc(shape, dtype, like, allocated):
-    t = torch.empty(shape, dtype=dtype, device=like.device)
+    # (from the cheapest call down: a small operator's time is mostly its outputs' allocation)
+    if dtype == like.dtype and shape == like.shape and like.is_contiguous():
+        t = torch.empty_like(like)
+    else:
+        t = like.new_empty(shape, dtype=dtype)
     allocated.append(t)
     return t
 

@@ -67,285 +67,278 @@ __device__ __forceinline__ uint2 encode8_group(const uint4& y, float s) {
 
 // ------------------------------------------------------- groups along rows
 
-// A row is held by `wpr` warps, CPL chunks of 8 elements per lane; a block
-// holds blockDim / 32 / wpr rows (a whole number).  A 1x128 group is 16
-// consecutive chunks, a half-warp, so only the row's sum of squares crosses
-// warps.  Any number of rows.  q == nullptr leaves the quantization out (s and
-// r only).  sum_out may be x or residual: every element is read and then
-// written by one thread.
-template <int CPL, int MAX_THREADS>
-__global__ void __launch_bounds__(MAX_THREADS)
+// Few rows: a block per row, CPL chunks of 8 elements per lane.  A 1x128
+// group is 16 consecutive chunks, a half-warp, so only the row's sum of squares
+// crosses warps.  q == nullptr leaves the quantization out (s and r only).
+// sum_out may be x or residual: every element is read and then written by one
+// thread.
+template <int CPL>
+__global__ void __launch_bounds__(1024)
     row_kernel(const uint4* x, const uint4* residual, const uint4* __restrict__ gamma, int64_t rows, int chunks,
-               float eps, int wpr, uint4* sum_out, float* __restrict__ rstd,
-               uint2* __restrict__ q, float* __restrict__ s_row) {
+               float eps, uint4* sum_out, float* __restrict__ rstd, uint2* __restrict__ q, float* __restrict__ s_row) {
     __shared__ double red[32];
+    const int lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5;
+    const int warps = blockDim.x >> 5;
+    const int64_t row = blockIdx.x;
+    const int64_t base = row * chunks;
+    const int c0 = warp * CPL * 32 + lane;
+    griddep_launch_dependents();
+    griddep_wait();                    // inputs of the preceding kernel are complete
+    uint4 s[CPL], e[CPL], g[CPL];
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+        const bool in = c0 + 32 * i < chunks;
+        s[i] = in ? x[base + c0 + 32 * i] : make_uint4(0u, 0u, 0u, 0u);
+        e[i] = in && residual ? residual[base + c0 + 32 * i] : make_uint4(0u, 0u, 0u, 0u);
+        g[i] = in && q ? __ldg(gamma + c0 + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    double sq = 0.0;
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) {
+        if (residual) {
+            s[i] = make_uint4(add2(s[i].x, e[i].x), add2(s[i].y, e[i].y), add2(s[i].z, e[i].z), add2(s[i].w, e[i].w));
+            if (c0 + 32 * i < chunks) sum_out[base + c0 + 32 * i] = s[i];
+        }
+        sq = sumsq2(s[i].w, sumsq2(s[i].z, sumsq2(s[i].y, sumsq2(s[i].x, sq))));
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+    if (warps > 1) {
+        if (lane == 0) red[warp] = sq;
+        __syncthreads();
+        sq = 0.0;
+        for (int w = 0; w < warps; ++w) sq += red[w];
+    }
+    const float r = rstd_of(sq, static_cast<int64_t>(chunks) * 8, eps);
+    if (threadIdx.x == 0) rstd[row] = r;
+    if (q) {
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) {
+            const int c = c0 + 32 * i;
+            const uint4 y = make_uint4(norm2(s[i].x, r, g[i].x), norm2(s[i].y, r, g[i].y), norm2(s[i].z, r, g[i].z),
+                                       norm2(s[i].w, r, g[i].w));
+            const float sc = group_scale(halfwarp_max(amax8_packed(y)));
+            if (c < chunks) {
+                q[base + c] = encode8_group(y, sc);
+                if ((lane & 15) == 0) s_row[static_cast<int64_t>(c >> 4) * rows + row] = sc;
+            }
+        }
+    }
+}
+
+// Many rows: a block stays and walks over rows, R per team at once, with the
+// loads of its next rows in flight while it works on these (R * CPL = 4 chunks
+// of x and of the residual per lane).  A row is held by `wpr` warps; a block has
+// blockDim / 32 / wpr such teams (a whole number).  Groups and aliasing as above;
+// red is double buffered, so one barrier per step keeps its readers and writers
+// apart.
+constexpr int kStreamThreads = 512;  // most threads of a block
+
+template <int CPL, int R>
+__global__ void __launch_bounds__(kStreamThreads, 1)
+    stream_kernel(const uint4* x, const uint4* residual, const uint4* __restrict__ gamma, int64_t rows, int chunks,
+                  float eps, int wpr, uint4* sum_out, float* __restrict__ rstd, uint2* __restrict__ q,
+                  float* __restrict__ s_row) {
+    __shared__ double red[2][kStreamThreads / 32][R];
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
     const int teams = (blockDim.x >> 5) / wpr;
     const int team = warp / wpr, tw = warp - team * wpr;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * teams + team;
+    const int c0 = tw * CPL * 32 + lane;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * teams * R;
+    int64_t row = (static_cast<int64_t>(blockIdx.x) * teams + team) * R;
+    griddep_launch_dependents();
     griddep_wait();                    // inputs of the preceding kernel are complete
-    if (row < rows) {                  // the same for a whole team
-        const int64_t base = row * chunks;
-        const int c0 = tw * CPL * 32 + lane;
-        uint4 s[CPL];
+
+    uint4 nx[R][CPL], ne[R][CPL];      // the next rows
+    auto fetch = [&](int64_t at) {
 #pragma unroll
-        for (int i = 0; i < CPL; ++i)
-            s[i] = (c0 + 32 * i < chunks) ? x[base + c0 + 32 * i] : make_uint4(0u, 0u, 0u, 0u);
-        if (residual) {
-            uint4 e[CPL];
-#pragma unroll
-            for (int i = 0; i < CPL; ++i)
-                e[i] = (c0 + 32 * i < chunks) ? residual[base + c0 + 32 * i] : make_uint4(0u, 0u, 0u, 0u);
+        for (int a = 0; a < R; ++a)
 #pragma unroll
             for (int i = 0; i < CPL; ++i) {
-                s[i] = make_uint4(add2(s[i].x, e[i].x), add2(s[i].y, e[i].y), add2(s[i].z, e[i].z), add2(s[i].w, e[i].w));
-                if (c0 + 32 * i < chunks) sum_out[base + c0 + 32 * i] = s[i];
+                const bool in = at + a < rows && c0 + 32 * i < chunks;
+                const int64_t k = (at + a) * chunks + c0 + 32 * i;
+                // (read once: s, which may be read again, is to stay in the cache)
+                nx[a][i] = in ? __ldcs(x + k) : make_uint4(0u, 0u, 0u, 0u);
+                ne[a][i] = in && residual ? __ldcs(residual + k) : make_uint4(0u, 0u, 0u, 0u);
+            }
+    };
+    fetch(row);
+    uint4 g[CPL];
+#pragma unroll
+    for (int i = 0; i < CPL; ++i) g[i] = q && c0 + 32 * i < chunks ? __ldg(gamma + c0 + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+
+    for (int buf = 0; row < rows; row += step, buf ^= 1) {      // the same for a whole team
+        uint4 s[R][CPL];
+#pragma unroll
+        for (int a = 0; a < R; ++a)
+#pragma unroll
+            for (int i = 0; i < CPL; ++i)
+                s[a][i] = residual ? make_uint4(add2(nx[a][i].x, ne[a][i].x), add2(nx[a][i].y, ne[a][i].y),
+                                                add2(nx[a][i].z, ne[a][i].z), add2(nx[a][i].w, ne[a][i].w))
+                                   : nx[a][i];
+        fetch(row + step);
+        double sq[R];
+#pragma unroll
+        for (int a = 0; a < R; ++a) {
+            sq[a] = 0.0;
+#pragma unroll
+            for (int i = 0; i < CPL; ++i) {
+                if (residual && row + a < rows && c0 + 32 * i < chunks) sum_out[(row + a) * chunks + c0 + 32 * i] = s[a][i];
+                sq[a] = sumsq2(s[a][i].w, sumsq2(s[a][i].z, sumsq2(s[a][i].y, sumsq2(s[a][i].x, sq[a]))));
             }
         }
-        double sq = 0.0;
 #pragma unroll
-        for (int i = 0; i < CPL; ++i) sq = sumsq2(s[i].w, sumsq2(s[i].z, sumsq2(s[i].y, sumsq2(s[i].x, sq))));
+        for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+            for (int a = 0; a < R; ++a) sq[a] += __shfl_xor_sync(0xffffffffu, sq[a], o);
         if (wpr > 1) {
-            if (lane == 0) red[warp] = sq;
+            if (lane == 0)
+#pragma unroll
+                for (int a = 0; a < R; ++a) red[buf][warp][a] = sq[a];
             named_bar_sync(1 + team, 32 * wpr);
-            sq = 0.0;
-            for (int w = 0; w < wpr; ++w) sq += red[team * wpr + w];
+#pragma unroll
+            for (int a = 0; a < R; ++a) {
+                sq[a] = 0.0;
+                for (int w = 0; w < wpr; ++w) sq[a] += red[buf][team * wpr + w][a];
+            }
         }
-        const float r = rstd_of(sq, static_cast<int64_t>(chunks) * 8, eps);
-        if (tw == 0 && lane == 0) rstd[row] = r;
-        if (q) {
+#pragma unroll
+        for (int a = 0; a < R; ++a) {
+            const float r = rstd_of(sq[a], static_cast<int64_t>(chunks) * 8, eps);
+            const bool live = row + a < rows;
+            if (tw == 0 && lane == 0 && live) rstd[row + a] = r;
+            if (!q) continue;
 #pragma unroll
             for (int i = 0; i < CPL; ++i) {
                 const int c = c0 + 32 * i;
-                const uint4 g = (c < chunks) ? __ldg(gamma + c) : make_uint4(0u, 0u, 0u, 0u);
-                const uint4 y = make_uint4(norm2(s[i].x, r, g.x), norm2(s[i].y, r, g.y), norm2(s[i].z, r, g.z),
-                                           norm2(s[i].w, r, g.w));
+                const uint4 v = s[a][i];
+                const uint4 y = make_uint4(norm2(v.x, r, g[i].x), norm2(v.y, r, g[i].y), norm2(v.z, r, g[i].z),
+                                           norm2(v.w, r, g[i].w));
                 const float sc = group_scale(halfwarp_max(amax8_packed(y)));
-                if (c < chunks) {
-                    q[base + c] = encode8_group(y, sc);
-                    if ((lane & 15) == 0) s_row[static_cast<int64_t>(c >> 4) * rows + row] = sc;
+                if (live && c < chunks) {
+                    q[(row + a) * chunks + c] = encode8_group(y, sc);
+                    if ((lane & 15) == 0) s_row[static_cast<int64_t>(c >> 4) * rows + row + a] = sc;
                 }
             }
         }
     }
-    griddep_launch_dependents();
 }
 
-// ------------------------------------------- groups along tokens (and rows)
+// ------------------------------------------------------- groups along tokens
 
-constexpr int kTileThreads = 512;
+// Codes and scales of y in 128x1 groups, from s and r: the second launch, which
+// finds s in the L2 cache where it was just written.  (One launch for
+// everything, a cluster of CTAs holding 128 rows in registers, took 43.6 us on
+// [8192, 2048]: its cluster-wide wait for the rows' statistics left loads,
+// arithmetic and stores one after the other.)
+//
+// A block has a 128 x 128 tile.  Warp w holds rows 16 w .. 16 w + 15, lane l
+// columns 4 l .. 4 l + 3, so loads are whole 256-byte runs of a row; the
+// columns' maxima meet in shared memory, and the codes are transposed there to
+// leave in 128-byte runs.
+constexpr int kColThreads = 256;
 
-// Rows of a value held by the lanes of a warp, 8 per lane, folded over the
-// warp: afterwards lane l holds (in v[0]) the fold of row fold_row(l) over
-// all 32 lanes.  Three halving steps exchange half of the rows each, two more
-// combine what is left.
-__device__ __forceinline__ int fold_row(int lane) { return ((lane >> 4) & 1) * 4 + ((lane >> 3) & 1) * 2 + ((lane >> 2) & 1); }
-__device__ __forceinline__ int fold_lane(int row) { return ((row >> 2) & 1) * 16 + ((row >> 1) & 1) * 8 + (row & 1) * 4; }
-
-template <typename T, typename Op>
-__device__ __forceinline__ T fold8(T (&v)[8], int lane, Op op) {
-#pragma unroll
-    for (int step = 0; step < 3; ++step) {
-        const int half = 4 >> step, mask = 16 >> step;
-        const bool up = (lane & mask) != 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            if (j < half) {
-                const T send = up ? v[j] : v[j + half];
-                const T keep = up ? v[j + half] : v[j];
-                v[j] = op(keep, __shfl_xor_sync(0xffffffffu, send, mask));
-            }
-        }
-    }
-    T a = v[0];
-    a = op(a, __shfl_xor_sync(0xffffffffu, a, 2));
-    return op(a, __shfl_xor_sync(0xffffffffu, a, 1));
-}
-
-__device__ __forceinline__ double ld_cluster_f64(uint32_t addr) {
-    double v;
-    asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
-    return v;
-}
-
-// A cluster of CTAs holds 128 rows; each CTA holds TPC tiles of 128 columns in
-// registers (tile `rank + k * ranks`, the last ones of some CTAs empty).  Warp
-// w holds rows 8 w .. 8 w + 7 of a tile, lane l columns 4 l .. 4 l + 3, so
-// loads, s and the row codes are whole 128- or 256-byte runs of a row.  The
-// CTAs exchange their rows' partial sums of squares through distributed shared
-// memory (added in rank order), and then each quantizes its own tiles: row
-// groups by shuffles, column groups through shared memory, the transposed
-// codes staged there to leave in 128-byte runs.
-template <int TPC>
-__global__ void __launch_bounds__(kTileThreads, TPC <= 2 ? 2 : 1)
-    tile_kernel(const __nv_bfloat16* x, const __nv_bfloat16* residual, const __nv_bfloat16* __restrict__ gamma,
-                int64_t rows, int64_t cols, float eps, int ranks, __nv_bfloat16* sum_out,
-                float* __restrict__ rstd, uint8_t* __restrict__ q_row,
-                float* __restrict__ s_row, uint8_t* __restrict__ q_colT, float* __restrict__ s_col) {
-    __shared__ double part[kGroup];
-    __shared__ float rrow[kGroup];
-    __shared__ __align__(16) uint2 colmax[16][32];       // [warp][lane]: maxima of 4 columns over 8 rows
+__global__ void __launch_bounds__(kColThreads, 4)
+    col_kernel(const __nv_bfloat16* __restrict__ s, const float* __restrict__ rstd,
+               const __nv_bfloat16* __restrict__ gamma, int64_t rows, int64_t cols, uint8_t* __restrict__ q_colT,
+               float* __restrict__ s_col) {
+    __shared__ __align__(16) uint2 colmax[8][32];        // [warp][lane]: maxima of 4 columns over 16 rows
     __shared__ float2 colq[kGroup];                      // a column's scale and its reciprocal
     __shared__ __align__(16) uint8_t stage[kGroup * kGroup];
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-    const int rank = static_cast<int>(cluster_ctarank());
-    const int64_t row0 = static_cast<int64_t>(blockIdx.x / ranks) * kGroup;
-    const int tiles = static_cast<int>(cols / kGroup);
-    griddep_wait();                    // inputs of the preceding kernel are complete
+    const int64_t tiles = cols / kGroup;
+    const int64_t block = blockIdx.x / tiles, tile = blockIdx.x - block * tiles;
+    const int64_t row0 = block * kGroup + 16 * warp, col0 = tile * kGroup;
+    griddep_launch_dependents();
+    griddep_wait();                    // s and r are complete
 
-    uint2 v[TPC][8];
-    double sq[8];
+    uint2 v[16];
+    const __nv_bfloat16* src = s + row0 * cols + col0 + 4 * lane;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sq[i] = 0.0;
+    for (int i = 0; i < 16; ++i) v[i] = __ldg(reinterpret_cast<const uint2*>(src + i * cols));
+    const uint2 g = __ldg(reinterpret_cast<const uint2*>(gamma + col0 + 4 * lane));
+    const float rl = __ldg(rstd + row0 + (lane & 15));
+    uint2 m = make_uint2(0u, 0u);
 #pragma unroll
-    for (int k = 0; k < TPC; ++k) {
-        const int tile = rank + k * ranks;
-        if (tile < tiles) {
-            const int64_t at = (row0 + 8 * warp) * cols + tile * kGroup + 4 * lane;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[k][i] = *reinterpret_cast<const uint2*>(x + at + i * cols);
-            if (residual) {
-                uint2 e[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) e[i] = *reinterpret_cast<const uint2*>(residual + at + i * cols);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    v[k][i] = make_uint2(add2(v[k][i].x, e[i].x), add2(v[k][i].y, e[i].y));
-                    *reinterpret_cast<uint2*>(sum_out + at + i * cols) = v[k][i];
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sq[i] = sumsq2(v[k][i].y, sumsq2(v[k][i].x, sq[i]));
-        }
+    for (int i = 0; i < 16; ++i) {
+        const float r = __shfl_sync(0xffffffffu, rl, i);
+        v[i] = make_uint2(norm2(v[i].x, r, g.x), norm2(v[i].y, r, g.y));
+        m = make_uint2(max2(m.x, abs2(v[i].x)), max2(m.y, abs2(v[i].y)));
     }
-    {
-        const double a = fold8(sq, lane, [](double p, double q) { return p + q; });
-        if ((lane & 3) == 0) part[8 * warp + fold_row(lane)] = a;
-    }
-    cluster_sync();                    // every rank's partial sums are in
-    if (t < kGroup) {
-        double a = 0.0;
-        const uint32_t mine = smem_u32(&part[t]);
-        for (int k = 0; k < ranks; ++k) a += ld_cluster_f64(map_to_cta(mine, static_cast<uint32_t>(k)));
-        const float r = rstd_of(a, cols, eps);
-        rrow[t] = r;
-        if (rank == 0) rstd[row0 + t] = r;
+    colmax[warp][lane] = m;
+    __syncthreads();
+    if (t < kGroup) {                  // column t of the tile
+        const uint16_t* cm = reinterpret_cast<const uint16_t*>(&colmax[0][0]) + t;
+        uint32_t a = 0;                // maxima of absolute values: their bits order like integers
+#pragma unroll
+        for (int w = 0; w < 8; ++w) a = max(a, static_cast<uint32_t>(cm[w * kGroup]));
+        const float sc = group_scale(__uint_as_float(a << 16));
+        colq[t] = make_float2(sc, __frcp_rn(sc));
+        s_col[block * cols + col0 + t] = sc;
     }
     __syncthreads();
-    // this CTA has read the others' sums; it leaves only when all have
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-
 #pragma unroll
-    for (int k = 0; k < TPC; ++k) {
-        const int tile = rank + k * ranks;
-        if (tile >= tiles) break;      // the same for the whole CTA
-        const uint2 g = __ldg(reinterpret_cast<const uint2*>(gamma + tile * kGroup + 4 * lane));
-        uint2 cm = make_uint2(0u, 0u);
-        uint32_t rm[8];
+    for (int j = 0; j < 4; ++j) {
+        const float2 c = colq[4 * lane + j];
+        const Quotient q(c.x, c.y);
+        uint32_t w[8];                 // two tokens of the column each
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float r = rrow[8 * warp + i];
-            v[k][i] = make_uint2(norm2(v[k][i].x, r, g.x), norm2(v[k][i].y, r, g.y));
-            const uint32_t a = abs2(v[k][i].x), b = abs2(v[k][i].y);
-            rm[i] = max2(a, b);
-            cm = make_uint2(max2(cm.x, a), max2(cm.y, b));
+            const uint32_t a = j < 2 ? v[2 * i].x : v[2 * i].y;
+            const uint32_t b = j < 2 ? v[2 * i + 1].x : v[2 * i + 1].y;
+            w[i] = __byte_perm(a, b, (j & 1) ? 0x7632 : 0x5410);
         }
-        if (q_colT) colmax[warp][lane] = cm;
-        if (q_row) {
-            const uint32_t m = fold8(rm, lane, [](uint32_t p, uint32_t q) { return max2(p, q); });
-            const float sc = group_scale(fmaxf(bf16_lo(m), bf16_hi(m)));
-            if ((lane & 3) == 0) s_row[static_cast<int64_t>(tile) * rows + row0 + 8 * warp + fold_row(lane)] = sc;
-            const float rc = __frcp_rn(sc);
+        uint4 o;
+        if (q.fast) {
+            const QuotientPair p(q, q);
+            o = make_uint4(p.codes(w[0]) | (p.codes(w[1]) << 16), p.codes(w[2]) | (p.codes(w[3]) << 16),
+                           p.codes(w[4]) | (p.codes(w[5]) << 16), p.codes(w[6]) | (p.codes(w[7]) << 16));
+        } else {
+            uint32_t* ow = reinterpret_cast<uint32_t*>(&o);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float si = __shfl_sync(0xffffffffu, sc, fold_lane(i));
-                const Quotient q(si, __shfl_sync(0xffffffffu, rc, fold_lane(i)));
-                uint32_t code;
-                if (q.fast) {
-                    const QuotientPair p(q, q);
-                    code = p.codes(v[k][i].x) | (p.codes(v[k][i].y) << 16);
-                } else {
-                    code = codes_pair_general(v[k][i].x, q, q) | (codes_pair_general(v[k][i].y, q, q) << 16);
-                }
-                *reinterpret_cast<uint32_t*>(q_row + (row0 + 8 * warp + i) * cols + tile * kGroup + 4 * lane) = code;
-            }
+            for (int i = 0; i < 4; ++i) ow[i] = codes_pair_general(w[2 * i], q, q) | (codes_pair_general(w[2 * i + 1], q, q) << 16);
         }
-        if (!q_colT) continue;
-        __syncthreads();
-        if (t < kGroup) {              // column t of the tile
-            const uint16_t* cmp = reinterpret_cast<const uint16_t*>(&colmax[0][0]) + t;
-            uint32_t m = 0;            // maxima of absolute values: their bits order like integers
-#pragma unroll
-            for (int w = 0; w < 16; ++w) m = max(m, static_cast<uint32_t>(cmp[w * kGroup]));
-            const float sc = group_scale(__uint_as_float(m << 16));
-            colq[t] = make_float2(sc, __frcp_rn(sc));
-            s_col[(row0 / kGroup) * cols + tile * kGroup + t] = sc;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 c = colq[4 * lane + j];
-            const Quotient q(c.x, c.y);
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t a = j < 2 ? v[k][2 * i].x : v[k][2 * i].y;
-                const uint32_t b = j < 2 ? v[k][2 * i + 1].x : v[k][2 * i + 1].y;
-                w[i] = __byte_perm(a, b, (j & 1) ? 0x7632 : 0x5410);    // two tokens of the column
-            }
-            uint2 o;
-            if (q.fast) {
-                const QuotientPair p(q, q);
-                o = make_uint2(p.codes(w[0]) | (p.codes(w[1]) << 16), p.codes(w[2]) | (p.codes(w[3]) << 16));
-            } else {
-                o = make_uint2(codes_pair_general(w[0], q, q) | (codes_pair_general(w[1], q, q) << 16),
-                               codes_pair_general(w[2], q, q) | (codes_pair_general(w[3], q, q) << 16));
-            }
-            // the column's 16 runs of 8 tokens, run w at w ^ (column / 4 % 16):
-            // the half-warp's 16 columns then fill all banks
-            *reinterpret_cast<uint2*>(stage + (4 * lane + j) * kGroup + ((warp ^ (lane & 15)) << 3)) = o;
-        }
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int u = t + i * kTileThreads;          // 16 bytes: column u / 8, tokens 16 (u % 8) ..
-            const int c = u >> 3, key = (c >> 2) & 15;
-            const uint4 o = *reinterpret_cast<const uint4*>(stage + c * kGroup + ((((u & 7) * 2) ^ (key & 14)) << 3));
-            const uint4 out = (key & 1) ? make_uint4(o.z, o.w, o.x, o.y) : o;
-            *reinterpret_cast<uint4*>(q_colT + (static_cast<int64_t>(tile) * kGroup + c) * rows + row0 + 16 * (u & 7)) = out;
-        }
+        // run w of 16 tokens at w ^ (column / 4 % 8): 8 lanes then fill all banks
+        *reinterpret_cast<uint4*>(stage + (4 * lane + j) * kGroup + ((warp ^ (lane & 7)) << 4)) = o;
     }
-    griddep_launch_dependents();
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int u = t + i * kColThreads;               // 16 bytes: column u / 8, tokens 16 (u % 8) ..
+        const int c = u >> 3;
+        const uint4 o = *reinterpret_cast<const uint4*>(stage + c * kGroup + (((u & 7) ^ ((c >> 2) & 7)) << 4));
+        *reinterpret_cast<uint4*>(q_colT + (col0 + c) * rows + block * kGroup + 16 * (u & 7)) = o;
+    }
 }
 
 // ------------------------------------------------------------------ gradient
 
-constexpr int kBwdThreads = 256;     // most threads of a block
+constexpr int kBwdThreads = 512;     // most threads of a block
 
 // A row is held by `wpr` warps, CPT chunks of 8 elements per lane; a block
-// has blockDim / 32 / wpr such teams (a whole number; several only with CPT ==
-// 1).  Each team walks over rows, R at once, keeping its columns' part of
-// dgamma in FP32 registers; the block's teams are added in order at the end
-// and leave as one row of `partial` (or as dgamma itself when the grid is one
-// block).  ds may be dy or dres: every element is read and then written by
-// one thread.
-template <int CPT, int R>
-__global__ void __launch_bounds__(kBwdThreads)
+// has blockDim / 32 / wpr such teams (a whole number; several only in blocks of
+// at most 256 threads and with CPT == 1).  Each team walks over rows, R at once,
+// the loads of its next rows in flight (AHEAD) while it works on these, keeping
+// its columns' part of dgamma in FP32 registers; the block's teams are added in
+// order at the end and leave as one row of `partial` (or as dgamma itself when
+// the grid is one block).  ds may be dy or dres: every element is read and then
+// written by one thread.
+template <int CPT, int R, bool AHEAD>
+__global__ void __launch_bounds__(kBwdThreads, 1)
     bwd_kernel(const uint4* dy, const uint4* __restrict__ s, const float* __restrict__ rstd,
                const uint4* __restrict__ gamma, const uint4* dres, int64_t rows, int chunks, int wpr, uint4* ds,
                float* __restrict__ partial, float* __restrict__ dgamma, int accumulate) {
     __shared__ float red[2][kBwdThreads / 32][R];
-    __shared__ float gsum[CPT == 1 ? kBwdThreads * 8 : 1];   // [team][column]
+    __shared__ float gsum[CPT == 1 ? 256 * 8 : 1];           // [team][column]
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
     const int teams = (blockDim.x >> 5) / wpr;
     const int team = warp / wpr, tw = warp - team * wpr;
     const int c0 = tw * CPT * 32 + lane;
     const float inv = 1.0f / (8.0f * static_cast<float>(chunks));
+    griddep_launch_dependents();
     griddep_wait();                    // inputs of the preceding kernel are complete
 
     uint4 gm[CPT];
@@ -357,23 +350,41 @@ __global__ void __launch_bounds__(kBwdThreads)
         for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
     }
     const int64_t step = static_cast<int64_t>(gridDim.x) * teams * R;
+    int64_t row = (static_cast<int64_t>(blockIdx.x) * teams + team) * R;
+    uint4 nd[R][CPT], ns[R][CPT], ne[R][CPT];    // the next rows
+    float nr[R];
+    auto fetch = [&](int64_t at) {
+#pragma unroll
+        for (int a = 0; a < R; ++a) {
+            const bool live = at + a < rows;
+            const int64_t base = (at + a) * chunks + c0;
+            nr[a] = live ? __ldg(rstd + at + a) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < CPT; ++i) {
+                const bool in = live && c0 + 32 * i < chunks;
+                nd[a][i] = in ? dy[base + 32 * i] : make_uint4(0u, 0u, 0u, 0u);
+                ns[a][i] = in ? __ldg(s + base + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+                ne[a][i] = in && dres ? dres[base + 32 * i] : make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+    };
+    if (AHEAD) fetch(row);
     int buf = 0;
-    for (int64_t row = (static_cast<int64_t>(blockIdx.x) * teams + team) * R; row < rows; row += step, buf ^= 1) {
+    for (; row < rows; row += step, buf ^= 1) {
+        if (!AHEAD) fetch(row);
         uint4 vd[R][CPT], vs[R][CPT], ve[R][CPT];
         float r[R], dot[R];
 #pragma unroll
         for (int a = 0; a < R; ++a) {
-            const bool live = row + a < rows;
-            const int64_t base = (row + a) * chunks + c0;
-            r[a] = live ? __ldg(rstd + row + a) : 0.0f;
+            r[a] = nr[a];
 #pragma unroll
             for (int i = 0; i < CPT; ++i) {
-                const bool in = live && c0 + 32 * i < chunks;
-                vd[a][i] = in ? dy[base + 32 * i] : make_uint4(0u, 0u, 0u, 0u);
-                vs[a][i] = in ? __ldg(s + base + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
-                ve[a][i] = in && dres ? dres[base + 32 * i] : make_uint4(0u, 0u, 0u, 0u);
+                vd[a][i] = nd[a][i];
+                vs[a][i] = ns[a][i];
+                ve[a][i] = ne[a][i];
             }
         }
+        if (AHEAD) fetch(row + step);
 #pragma unroll
         for (int a = 0; a < R; ++a) {
             dot[a] = 0.0f;
@@ -459,7 +470,6 @@ __global__ void __launch_bounds__(kBwdThreads)
                     }
         }
     }
-    griddep_launch_dependents();
 }
 
 // dgamma (+)= the sum of the blocks' partial rows, in a fixed order: 32
@@ -469,6 +479,7 @@ __global__ void __launch_bounds__(256) dgamma_kernel(const float* __restrict__ p
     __shared__ float sums[8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
+    griddep_launch_dependents();
     griddep_wait();
     float a = 0.0f;
 #pragma unroll 8
@@ -480,7 +491,6 @@ __global__ void __launch_bounds__(256) dgamma_kernel(const float* __restrict__ p
         for (int w = 1; w < 8; ++w) a += sums[w][lane];
         dgamma[c] = accumulate ? dgamma[c] + a : a;
     }
-    griddep_launch_dependents();
 }
 
 }  // namespace addnorm

@@ -378,16 +378,29 @@ cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, 
 }
 
 // add + RMSNorm (+ row-wise quantization when q is given): one launch.
-template <int CPL, int MAX_THREADS>
+template <int CPL, int R>
+cudaError_t launch_norm_stream(const void* x, const void* residual, const void* gamma, int64_t rows, int chunks,
+                               float eps, void* sum_out, float* rstd, uint8_t* q, float* s_row, int sms,
+                               cudaStream_t stream) {
+    const int wpr = (chunks + 32 * CPL - 1) / (32 * CPL);
+    const int teams = wpr < 8 ? 8 / wpr : 1;
+    const int threads = 32 * wpr * teams;
+    const int64_t need = (rows + teams * R - 1) / (teams * R), cap = static_cast<int64_t>(sms) * (addnorm::kStreamThreads / threads);
+    const int64_t each = (need + cap - 1) / cap;         // steps of the busiest block; the others' about as many
+    return launch_pdl(addnorm::stream_kernel<CPL, R>, dim3(static_cast<unsigned>((need + each - 1) / each)),
+                      dim3(static_cast<unsigned>(threads)), 0, stream, static_cast<const uint4*>(x),
+                      static_cast<const uint4*>(residual), static_cast<const uint4*>(gamma), rows, chunks, eps, wpr,
+                      static_cast<uint4*>(sum_out), rstd, reinterpret_cast<uint2*>(q), s_row);
+}
+
+// Few rows: one step per block.
+template <int CPL>
 cudaError_t launch_norm_rows(const void* x, const void* residual, const void* gamma, int64_t rows, int chunks,
                              float eps, void* sum_out, float* rstd, uint8_t* q, float* s_row, cudaStream_t stream) {
     const int wpr = (chunks + 32 * CPL - 1) / (32 * CPL);
-    int teams = MAX_THREADS == 256 ? 8 / wpr : 1;
-    if (teams > rows) teams = static_cast<int>(rows);
-    const unsigned grid = static_cast<unsigned>((rows + teams - 1) / teams);
-    return launch_pdl(addnorm::row_kernel<CPL, MAX_THREADS>, dim3(grid), dim3(32 * wpr * teams), 0, stream,
+    return launch_pdl(addnorm::row_kernel<CPL>, dim3(static_cast<unsigned>(rows)), dim3(32 * wpr), 0, stream,
                       static_cast<const uint4*>(x), static_cast<const uint4*>(residual),
-                      static_cast<const uint4*>(gamma), rows, chunks, eps, wpr, static_cast<uint4*>(sum_out), rstd,
+                      static_cast<const uint4*>(gamma), rows, chunks, eps, static_cast<uint4*>(sum_out), rstd,
                       reinterpret_cast<uint2*>(q), s_row);
 }
 
@@ -400,41 +413,33 @@ fp8_status norm_rows(const void* x, const void* residual, const void* gamma, int
     const int chunks = static_cast<int>(cols / 8);
     cudaError_t e;
     // Few rows: a row over as many warps as it has 512-byte runs, so that a
-    // token's latency is one load and one short pass.  Many rows: up to 64
-    // elements per lane, which leaves the reductions to shuffles.
+    // token's latency is one load and one short pass.  Many rows: 4 chunks per
+    // lane and step, of as few rows as that takes.
     if (rows <= 2 * sms && chunks <= 1024)
-        e = launch_norm_rows<1, 1024>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, s);
+        e = launch_norm_rows<1>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, s);
     else if (rows <= 2 * sms)
-        e = launch_norm_rows<2, 1024>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, s);
+        e = launch_norm_rows<2>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, s);
     else if (chunks <= 32)
-        e = launch_norm_rows<1, 256>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, s);
+        e = launch_norm_stream<1, 4>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, sms, s);
     else if (chunks <= 64)
-        e = launch_norm_rows<2, 256>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, s);
-    else if (chunks <= 128)
-        e = launch_norm_rows<4, 256>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, s);
+        e = launch_norm_stream<2, 2>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, sms, s);
     else
-        e = launch_norm_rows<8, 256>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, s);
+        e = launch_norm_stream<4, 1>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, sms, s);
     if (e != cudaSuccess) return cuda_fail("add + rmsnorm launch", e);
     return last_launch_status("add + rmsnorm launch");
 }
 
-template <int TPC>
-fp8_status norm_tiles(const void* x, const void* residual, const void* gamma, int64_t rows, int64_t cols, float eps,
-                      void* sum_out, float* rstd, uint8_t* q_row, float* s_row, uint8_t* q_colT, float* s_col,
-                      cudaStream_t s) {
-    const int tiles = static_cast<int>(cols / 128);
-    const int ranks = (tiles + TPC - 1) / TPC;
-    const cudaError_t e = launch_pdl_cluster(
-        addnorm::tile_kernel<TPC>, dim3(static_cast<unsigned>(rows / 128 * ranks)), dim3(addnorm::kTileThreads),
-        static_cast<unsigned>(ranks), s, static_cast<const __nv_bfloat16*>(x),
-        static_cast<const __nv_bfloat16*>(residual), static_cast<const __nv_bfloat16*>(gamma), rows, cols, eps, ranks,
-        static_cast<__nv_bfloat16*>(sum_out), rstd, q_row, s_row, q_colT, s_col);
-    if (e != cudaSuccess) return cuda_fail("add + rmsnorm tile launch", e);
-    return last_launch_status("add + rmsnorm tile launch");
+fp8_status norm_cols(const void* sum, const float* rstd, const void* gamma, int64_t rows, int64_t cols,
+                     uint8_t* q_colT, float* s_col, cudaStream_t s) {
+    const cudaError_t e = launch_pdl(addnorm::col_kernel, dim3(static_cast<unsigned>((rows / 128) * (cols / 128))),
+                                     dim3(addnorm::kColThreads), 0, s, static_cast<const __nv_bfloat16*>(sum), rstd,
+                                     static_cast<const __nv_bfloat16*>(gamma), rows, cols, q_colT, s_col);
+    if (e != cudaSuccess) return cuda_fail("rmsnorm column groups launch", e);
+    return last_launch_status("rmsnorm column groups launch");
 }
 
-// Blocks of the norm's gradient: as many as can be resident (two per SM), each
-// of which leaves one row of dgamma's partial sums.
+// Blocks of the norm's gradient: at most as many as can be resident, with
+// equal shares of the rows; each leaves one row of dgamma's partial sums.
 struct BwdShape {
     int chunks, cpt, wpr, teams, rows_at_once;
     unsigned grid;
@@ -442,21 +447,23 @@ struct BwdShape {
 BwdShape norm_bwd_shape(int64_t rows, int64_t cols, int sms) {
     BwdShape b;
     b.chunks = static_cast<int>(cols / 8);
-    b.cpt = b.chunks <= 256 ? 1 : b.chunks <= 512 ? 2 : b.chunks <= 1024 ? 4 : 8;
+    b.cpt = b.chunks <= 512 ? 1 : b.chunks <= 1024 ? 2 : 4;
     b.rows_at_once = b.cpt == 1 ? 2 : 1;
     b.wpr = (b.chunks + 32 * b.cpt - 1) / (32 * b.cpt);
-    b.teams = b.cpt == 1 ? (addnorm::kBwdThreads / 32) / b.wpr : 1;
+    b.teams = b.cpt == 1 && b.wpr < 8 ? 8 / b.wpr : 1;
     const int64_t per = static_cast<int64_t>(b.teams) * b.rows_at_once;
-    const int64_t need = (rows + per - 1) / per, cap = 2 * static_cast<int64_t>(sms);
-    b.grid = static_cast<unsigned>(need < cap ? need : cap);
+    const int64_t need = (rows + per - 1) / per;
+    const int64_t cap = static_cast<int64_t>(sms) * (addnorm::kBwdThreads / (32 * b.wpr * b.teams));
+    const int64_t each = (need + cap - 1) / cap;
+    b.grid = static_cast<unsigned>((need + each - 1) / each);
     return b;
 }
 
-template <int CPT, int R>
+template <int CPT, int R, bool AHEAD>
 cudaError_t launch_norm_bwd(const BwdShape& b, const void* dy, const void* x, const float* rstd, const void* gamma,
                             const void* dres, int64_t rows, void* ds, float* partial, float* dgamma, int accumulate,
                             cudaStream_t s) {
-    return launch_pdl(addnorm::bwd_kernel<CPT, R>, dim3(b.grid), dim3(32 * b.wpr * b.teams), 0, s,
+    return launch_pdl(addnorm::bwd_kernel<CPT, R, AHEAD>, dim3(b.grid), dim3(32 * b.wpr * b.teams), 0, s,
                       static_cast<const uint4*>(dy), static_cast<const uint4*>(x), rstd,
                       static_cast<const uint4*>(gamma), static_cast<const uint4*>(dres), rows, b.chunks, b.wpr,
                       static_cast<uint4*>(ds), partial, dgamma, accumulate);
@@ -766,25 +773,10 @@ fp8_status fp8_add_rmsnorm_quantize_1x128(const void* x_bf16, const void* residu
     if ((mode & FP8_ROWWISE) && (!aligned16(q_row) || !aligned16(s_row))) return FP8_ERR_ALIGN;
     if ((mode & FP8_COLWISE) && (!aligned16(q_colT) || !aligned16(s_col))) return FP8_ERR_ALIGN;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (mode == FP8_ROWWISE)
-        return norm_rows(x_bf16, residual_bf16, gamma_bf16, rows, cols, eps, sum_bf16, rstd, q_row, s_row, s);
-    if (mode == FP8_COLWISE) q_row = nullptr;
-    if (cols <= 8 * 128)
-        return norm_tiles<1>(x_bf16, residual_bf16, gamma_bf16, rows, cols, eps, sum_bf16, rstd, q_row, s_row, q_colT,
-                             s_col, s);
-    if (cols <= 16 * 128)
-        return norm_tiles<2>(x_bf16, residual_bf16, gamma_bf16, rows, cols, eps, sum_bf16, rstd, q_row, s_row, q_colT,
-                             s_col, s);
-    if (cols <= 32 * 128)
-        return norm_tiles<4>(x_bf16, residual_bf16, gamma_bf16, rows, cols, eps, sum_bf16, rstd, q_row, s_row, q_colT,
-                             s_col, s);
-    // Wider rows do not fit a cluster's registers: the sum and the statistic
-    // first, then the tile quantizer on the sum.
-    const fp8_status st = norm_rows(x_bf16, residual_bf16, gamma_bf16, rows, cols, eps, sum_bf16, rstd, nullptr,
-                                    nullptr, s);
-    if (st != FP8_OK) return st;
-    return fp8_rmsnorm_quantize_1x128(residual_bf16 ? sum_bf16 : x_bf16, rows, cols, rstd, gamma_bf16, mode, q_row,
-                                      s_row, q_colT, s_col, stream);
+    if (!(mode & FP8_ROWWISE)) q_row = nullptr;
+    const fp8_status st = norm_rows(x_bf16, residual_bf16, gamma_bf16, rows, cols, eps, sum_bf16, rstd, q_row, s_row, s);
+    if (st != FP8_OK || mode == FP8_ROWWISE) return st;
+    return norm_cols(residual_bf16 ? sum_bf16 : x_bf16, rstd, gamma_bf16, rows, cols, q_colT, s_col, s);
 }
 
 fp8_status fp8_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols, size_t* bytes) {
@@ -834,17 +826,14 @@ fp8_status fp8_rmsnorm_backward(const void* dy_bf16, const void* s_bf16, const f
     float* partial = static_cast<float*>(workspace);
     cudaError_t e;
     if (b.cpt == 1)
-        e = launch_norm_bwd<1, 2>(b, dy_bf16, s_bf16, rstd, gamma_bf16, dresidual_bf16, rows, ds_bf16, partial,
-                                  dgamma_f32, accumulate, s);
+        e = launch_norm_bwd<1, 2, true>(b, dy_bf16, s_bf16, rstd, gamma_bf16, dresidual_bf16, rows, ds_bf16, partial,
+                                        dgamma_f32, accumulate, s);
     else if (b.cpt == 2)
-        e = launch_norm_bwd<2, 1>(b, dy_bf16, s_bf16, rstd, gamma_bf16, dresidual_bf16, rows, ds_bf16, partial,
-                                  dgamma_f32, accumulate, s);
-    else if (b.cpt == 4)
-        e = launch_norm_bwd<4, 1>(b, dy_bf16, s_bf16, rstd, gamma_bf16, dresidual_bf16, rows, ds_bf16, partial,
-                                  dgamma_f32, accumulate, s);
-    else
-        e = launch_norm_bwd<8, 1>(b, dy_bf16, s_bf16, rstd, gamma_bf16, dresidual_bf16, rows, ds_bf16, partial,
-                                  dgamma_f32, accumulate, s);
+        e = launch_norm_bwd<2, 1, true>(b, dy_bf16, s_bf16, rstd, gamma_bf16, dresidual_bf16, rows, ds_bf16, partial,
+                                        dgamma_f32, accumulate, s);
+    else                               // (its registers do not hold two rows' chunks)
+        e = launch_norm_bwd<4, 1, false>(b, dy_bf16, s_bf16, rstd, gamma_bf16, dresidual_bf16, rows, ds_bf16, partial,
+                                         dgamma_f32, accumulate, s);
     if (e != cudaSuccess) return cuda_fail("rmsnorm backward launch", e);
     if ((st = last_launch_status("rmsnorm backward launch")) != FP8_OK) return st;
     if (dgamma_f32 && b.grid > 1) {

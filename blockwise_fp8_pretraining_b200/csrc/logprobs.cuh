@@ -338,6 +338,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
         else
             __syncthreads();
     };
+    griddep_launch_dependents();
     griddep_wait();                    // inputs of the preceding kernel are complete
     if (row >= rows) return;           // (a whole warp of its own)
 
@@ -562,7 +563,6 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
             top_index[row * topk + lane] = k == 0 ? -1 : static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(k));
         }
     }
-    griddep_launch_dependents();
     __syncwarp();
     if (ranks > 1) cluster_wait();
 }
@@ -582,6 +582,7 @@ __global__ void __launch_bounds__(kMaxThreads, 3)
                     const float* __restrict__ entropy, const float* __restrict__ dentropy, int64_t chunks, T* dlogits,
                     int64_t ld_out) {
     using E = Elem<T>;
+    griddep_launch_dependents();
     griddep_wait();                    // inputs of the preceding kernel are complete
     const int64_t row = blockIdx.x / chunks, chunk = blockIdx.x - row * chunks;
     const T* x = logits + row * ld;
@@ -651,7 +652,6 @@ __global__ void __launch_bounds__(kMaxThreads, 3)
     }
     if (chunk == 0 && threadIdx.x < head) single(threadIdx.x);
     if (chunk == chunks - 1 && threadIdx.x < vocab - tail0) single(tail0 + threadIdx.x);
-    griddep_launch_dependents();
 }
 
 }  // namespace logp

@@ -50,8 +50,27 @@ __device__ __forceinline__ uint32_t norm2(uint32_t s, float r, uint32_t gamma) {
     return as_u32(__hmul2_rn(as_bf162(gamma), t));
 }
 
+// fp32(1 / sqrt(sum / cols + eps)).  Inside FP32's range one Newton step in FP64
+// from rsqrtf's answer (off by 2^-22 at most) leaves a relative error of 3/2
+// 2^-44: the rounding to FP32 then differs from the exact value's in one of a
+// million rows, by one unit.  (Every lane computes it; the division and square
+// root in FP64 were a fifth of the kernel's instructions.)
 __device__ __forceinline__ float rstd_of(double sum, int64_t cols, float eps) {
-    return static_cast<float>(1.0 / sqrt(sum / static_cast<double>(cols) + static_cast<double>(eps)));
+    const double v = fma(sum, 1.0 / static_cast<double>(cols), static_cast<double>(eps));
+    if (v > 1e-30 && v < 1e30) {
+        const double y = rsqrtf(static_cast<float>(v));
+        return static_cast<float>(fma(0.5 * y, fma(-v * y, y, 1.0), y));
+    }
+    return static_cast<float>(1.0 / sqrt(v));
+}
+
+// amax / 448 rounded to nearest, as group_scale: the residual of the product
+// with RN(1 / 448) corrects it (exact as long as nothing underflows).
+__device__ __forceinline__ float scale_of(float amax) {
+    if (amax < 0x1p-100f) return group_scale(amax);
+    constexpr float r = 1.0f / 448.0f;
+    const float q = amax * r;
+    return fmaf(fmaf(-448.0f, q, amax), r, q);
 }
 
 // Codes of the 8 values of a chunk, one scale.
@@ -118,7 +137,7 @@ __global__ void __launch_bounds__(1024)
             const int c = c0 + 32 * i;
             const uint4 y = make_uint4(norm2(s[i].x, r, g[i].x), norm2(s[i].y, r, g[i].y), norm2(s[i].z, r, g[i].z),
                                        norm2(s[i].w, r, g[i].w));
-            const float sc = group_scale(halfwarp_max(amax8_packed(y)));
+            const float sc = scale_of(halfwarp_max(amax8_packed(y)));
             if (c < chunks) {
                 q[base + c] = encode8_group(y, sc);
                 if ((lane & 15) == 0) s_row[static_cast<int64_t>(c >> 4) * rows + row] = sc;
@@ -128,19 +147,21 @@ __global__ void __launch_bounds__(1024)
 }
 
 // Many rows: a block stays and walks over rows, R per team at once, with the
-// loads of its next rows in flight while it works on these (R * CPL = 4 chunks
-// of x and of the residual per lane).  A row is held by `wpr` warps; a block has
+// loads of its next rows in flight while it works on these (R * CPL = 2 or 4
+// chunks of x and of the residual per lane: 2 leave room for 24 warps per SM, 4
+// hold longer rows with 16).  A row is held by `wpr` warps; a block has
 // blockDim / 32 / wpr such teams (a whole number).  Groups and aliasing as above;
 // red is double buffered, so one barrier per step keeps its readers and writers
 // apart.
-constexpr int kStreamThreads = 512;  // most threads of a block
+template <int CPL, int R> constexpr int kStreamThreads = CPL * R == 2 ? 384 : 512;   // most threads of a block
+template <int CPL, int R> constexpr int kStreamBlocks = CPL * R == 2 ? 2 : 1;         // of which an SM holds these
 
 template <int CPL, int R>
-__global__ void __launch_bounds__(kStreamThreads, 1)
+__global__ void __launch_bounds__(kStreamThreads<CPL, R>, kStreamBlocks<CPL, R>)
     stream_kernel(const uint4* x, const uint4* residual, const uint4* __restrict__ gamma, int64_t rows, int chunks,
                   float eps, int wpr, uint4* sum_out, float* __restrict__ rstd, uint2* __restrict__ q,
                   float* __restrict__ s_row) {
-    __shared__ double red[2][kStreamThreads / 32][R];
+    __shared__ double red[2][kStreamThreads<CPL, R> / 32][R];
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
     const int teams = (blockDim.x >> 5) / wpr;
@@ -151,17 +172,24 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
     griddep_launch_dependents();
     griddep_wait();                    // inputs of the preceding kernel are complete
 
-    uint4 nx[R][CPL], ne[R][CPL];      // the next rows
+    // The next rows.  Lanes behind a row's end hold zeros throughout; rows behind
+    // the last hold what was there (they are worked on and left unstored).
+    uint4 nx[R][CPL], ne[R][CPL];
+#pragma unroll
+    for (int a = 0; a < R; ++a)
+#pragma unroll
+        for (int i = 0; i < CPL; ++i) nx[a][i] = ne[a][i] = make_uint4(0u, 0u, 0u, 0u);
     auto fetch = [&](int64_t at) {
 #pragma unroll
         for (int a = 0; a < R; ++a)
 #pragma unroll
             for (int i = 0; i < CPL; ++i) {
-                const bool in = at + a < rows && c0 + 32 * i < chunks;
-                const int64_t k = (at + a) * chunks + c0 + 32 * i;
-                // (read once: s, which may be read again, is to stay in the cache)
-                nx[a][i] = in ? __ldcs(x + k) : make_uint4(0u, 0u, 0u, 0u);
-                ne[a][i] = in && residual ? __ldcs(residual + k) : make_uint4(0u, 0u, 0u, 0u);
+                if (at + a < rows && c0 + 32 * i < chunks) {
+                    const int64_t k = (at + a) * chunks + c0 + 32 * i;
+                    // (read once: s, which may be read again, is to stay in the cache)
+                    nx[a][i] = __ldcs(x + k);
+                    if (residual) ne[a][i] = __ldcs(residual + k);
+                }
             }
     };
     fetch(row);
@@ -216,7 +244,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1)
                 const uint4 v = s[a][i];
                 const uint4 y = make_uint4(norm2(v.x, r, g[i].x), norm2(v.y, r, g[i].y), norm2(v.z, r, g[i].z),
                                            norm2(v.w, r, g[i].w));
-                const float sc = group_scale(halfwarp_max(amax8_packed(y)));
+                const float sc = scale_of(halfwarp_max(amax8_packed(y)));
                 if (live && c < chunks) {
                     q[(row + a) * chunks + c] = encode8_group(y, sc);
                     if ((lane & 15) == 0) s_row[static_cast<int64_t>(c >> 4) * rows + row + a] = sc;
@@ -274,7 +302,7 @@ __global__ void __launch_bounds__(kColThreads, 4)
         uint32_t a = 0;                // maxima of absolute values: their bits order like integers
 #pragma unroll
         for (int w = 0; w < 8; ++w) a = max(a, static_cast<uint32_t>(cm[w * kGroup]));
-        const float sc = group_scale(__uint_as_float(a << 16));
+        const float sc = scale_of(__uint_as_float(a << 16));
         colq[t] = make_float2(sc, __frcp_rn(sc));
         s_col[block * cols + col0 + t] = sc;
     }
@@ -331,7 +359,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                const uint4* __restrict__ gamma, const uint4* dres, int64_t rows, int chunks, int wpr, uint4* ds,
                float* __restrict__ partial, float* __restrict__ dgamma, int accumulate) {
     __shared__ float red[2][kBwdThreads / 32][R];
-    __shared__ float gsum[CPT == 1 ? 256 * 8 : 1];           // [team][column]
+    __shared__ __align__(16) float gsum[CPT == 1 ? 256 * 8 : 2];          // [team][column]
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
     const int teams = (blockDim.x >> 5) / wpr;
@@ -341,18 +369,30 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     griddep_launch_dependents();
     griddep_wait();                    // inputs of the preceding kernel are complete
 
-    uint4 gm[CPT];
-    float acc[CPT][8];
+    // AHEAD: n = s r, gamma dy and gamma stay unpacked, as the next rows take the
+    // loads' registers; else everything is unpacked where it is used.
+    uint4 gp[CPT];
+    float2 gm[CPT][4], acc[CPT][4];
 #pragma unroll
     for (int i = 0; i < CPT; ++i) {
-        gm[i] = (c0 + 32 * i < chunks) ? __ldg(gamma + c0 + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+        gp[i] = (c0 + 32 * i < chunks) ? __ldg(gamma + c0 + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t w[4] = {gp[i].x, gp[i].y, gp[i].z, gp[i].w};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = 0.0f;
+        for (int j = 0; j < 4; ++j) {
+            gm[i][j] = unpack_bf16x2(w[j]);
+            acc[i][j] = make_float2(0.0f, 0.0f);
+        }
     }
     const int64_t step = static_cast<int64_t>(gridDim.x) * teams * R;
     int64_t row = (static_cast<int64_t>(blockIdx.x) * teams + team) * R;
-    uint4 nd[R][CPT], ns[R][CPT], ne[R][CPT];    // the next rows
+    // The next rows.  Lanes behind a row's end hold zeros throughout; a row behind
+    // the last has rstd = 0, which takes it out of dgamma.
+    uint4 nd[R][CPT], ns[R][CPT], ne[R][CPT];
     float nr[R];
+#pragma unroll
+    for (int a = 0; a < R; ++a)
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) nd[a][i] = ns[a][i] = ne[a][i] = make_uint4(0u, 0u, 0u, 0u);
     auto fetch = [&](int64_t at) {
 #pragma unroll
         for (int a = 0; a < R; ++a) {
@@ -361,10 +401,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             nr[a] = live ? __ldg(rstd + at + a) : 0.0f;
 #pragma unroll
             for (int i = 0; i < CPT; ++i) {
-                const bool in = live && c0 + 32 * i < chunks;
-                nd[a][i] = in ? dy[base + 32 * i] : make_uint4(0u, 0u, 0u, 0u);
-                ns[a][i] = in ? __ldg(s + base + 32 * i) : make_uint4(0u, 0u, 0u, 0u);
-                ne[a][i] = in && dres ? dres[base + 32 * i] : make_uint4(0u, 0u, 0u, 0u);
+                if (live && c0 + 32 * i < chunks) {
+                    nd[a][i] = dy[base + 32 * i];
+                    ns[a][i] = __ldg(s + base + 32 * i);
+                    if (dres) ne[a][i] = dres[base + 32 * i];
+                } else if (R > 1) {        // (its values, NaN among them, must not meet rstd = 0)
+                    nd[a][i] = ns[a][i] = make_uint4(0u, 0u, 0u, 0u);
+                }
             }
         }
     };
@@ -372,37 +415,35 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     int buf = 0;
     for (; row < rows; row += step, buf ^= 1) {
         if (!AHEAD) fetch(row);
-        uint4 vd[R][CPT], vs[R][CPT], ve[R][CPT];
+        float2 n[R][CPT][4], gd[R][CPT][4];      // s r and gamma dy
+        uint4 ve[R][CPT];
         float r[R], dot[R];
 #pragma unroll
         for (int a = 0; a < R; ++a) {
             r[a] = nr[a];
+            float2 dots = make_float2(0.0f, 0.0f);
+            const float2 r2 = make_float2(r[a], r[a]);
 #pragma unroll
             for (int i = 0; i < CPT; ++i) {
-                vd[a][i] = nd[a][i];
-                vs[a][i] = ns[a][i];
-                ve[a][i] = ne[a][i];
-            }
-        }
-        if (AHEAD) fetch(row + step);
-#pragma unroll
-        for (int a = 0; a < R; ++a) {
-            dot[a] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < CPT; ++i) {
-                const uint32_t* dw = reinterpret_cast<const uint32_t*>(&vd[a][i]);
-                const uint32_t* sw = reinterpret_cast<const uint32_t*>(&vs[a][i]);
-                const uint32_t* gw = reinterpret_cast<const uint32_t*>(&gm[i]);
+                const uint32_t dw[4] = {nd[a][i].x, nd[a][i].y, nd[a][i].z, nd[a][i].w};
+                const uint32_t sw[4] = {ns[a][i].x, ns[a][i].y, ns[a][i].z, ns[a][i].w};
+                const uint32_t gw[4] = {gp[i].x, gp[i].y, gp[i].z, gp[i].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 d = unpack_bf16x2(dw[j]), f = unpack_bf16x2(sw[j]), g = unpack_bf16x2(gw[j]);
-                    const float p0 = d.x * (f.x * r[a]), p1 = d.y * (f.y * r[a]);    // dy n
-                    acc[i][2 * j] += p0;
-                    acc[i][2 * j + 1] += p1;
-                    dot[a] = fmaf(g.y, p1, fmaf(g.x, p0, dot[a]));
+                    const float2 dv = unpack_bf16x2(dw[j]), nv = __fmul2_rn(unpack_bf16x2(sw[j]), r2);
+                    const float2 gv = __fmul2_rn(AHEAD ? gm[i][j] : unpack_bf16x2(gw[j]), dv);
+                    acc[i][j] = __ffma2_rn(dv, nv, acc[i][j]);
+                    dots = __ffma2_rn(gv, nv, dots);
+                    if (AHEAD) {
+                        n[a][i][j] = nv;
+                        gd[a][i][j] = gv;
+                    }
                 }
+                if (AHEAD) ve[a][i] = ne[a][i];
             }
+            dot[a] = dots.x + dots.y;
         }
+        if (AHEAD) fetch(row + step);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
@@ -420,20 +461,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         }
 #pragma unroll
         for (int a = 0; a < R; ++a) {
-            const float m = dot[a] * inv;
+            const float m = -dot[a] * inv;
+            const float2 m2 = make_float2(m, m), r2 = make_float2(r[a], r[a]);
 #pragma unroll
             for (int i = 0; i < CPT; ++i) {
-                const uint32_t* dw = reinterpret_cast<const uint32_t*>(&vd[a][i]);
-                const uint32_t* sw = reinterpret_cast<const uint32_t*>(&vs[a][i]);
-                const uint32_t* ew = reinterpret_cast<const uint32_t*>(&ve[a][i]);
-                const uint32_t* gw = reinterpret_cast<const uint32_t*>(&gm[i]);
+                const uint4 e = AHEAD ? ve[a][i] : ne[a][i];
+                const uint32_t ew[4] = {e.x, e.y, e.z, e.w};
+                const uint32_t dw[4] = {nd[a][i].x, nd[a][i].y, nd[a][i].z, nd[a][i].w};
+                const uint32_t sw[4] = {ns[a][i].x, ns[a][i].y, ns[a][i].z, ns[a][i].w};
+                const uint32_t gw[4] = {gp[i].x, gp[i].y, gp[i].z, gp[i].w};
                 uint32_t o[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float2 d = unpack_bf16x2(dw[j]), f = unpack_bf16x2(sw[j]), g = unpack_bf16x2(gw[j]),
-                                 e = unpack_bf16x2(ew[j]);
-                    const float a0 = fmaf(-(f.x * r[a]), m, g.x * d.x), a1 = fmaf(-(f.y * r[a]), m, g.y * d.y);
-                    o[j] = as_u32(__floats2bfloat162_rn(fmaf(r[a], a0, e.x), fmaf(r[a], a1, e.y)));
+                    const float2 nv = AHEAD ? n[a][i][j] : __fmul2_rn(unpack_bf16x2(sw[j]), r2);
+                    const float2 gv = AHEAD ? gd[a][i][j] : __fmul2_rn(unpack_bf16x2(gw[j]), unpack_bf16x2(dw[j]));
+                    const float2 v = __ffma2_rn(r2, __ffma2_rn(nv, m2, gv), unpack_bf16x2(ew[j]));
+                    o[j] = as_u32(__floats2bfloat162_rn(v.x, v.y));
                 }
                 if (row + a < rows && c0 + 32 * i < chunks)
                     ds[(row + a) * chunks + c0 + 32 * i] = make_uint4(o[0], o[1], o[2], o[3]);
@@ -447,7 +490,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (CPT == 1 && teams > 1) {
             if (c0 < chunks)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) gsum[team * cols + 8 * c0 + j] = acc[0][j];
+                for (int j = 0; j < 4; ++j) *reinterpret_cast<float2*>(&gsum[team * cols + 8 * c0 + 2 * j]) = acc[0][j];
             __syncthreads();
             for (int c = threadIdx.x; c < cols; c += blockDim.x) {
                 float a = 0.0f;
@@ -459,9 +502,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             for (int i = 0; i < CPT; ++i)
                 if (c0 + 32 * i < chunks)
 #pragma unroll
-                    for (int j = 0; j < 8; j += 4) {
-                        float4* o = reinterpret_cast<float4*>(out + 8 * (c0 + 32 * i) + j);
-                        float4 a = make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
+                    for (int j = 0; j < 4; j += 2) {
+                        float4* o = reinterpret_cast<float4*>(out + 8 * (c0 + 32 * i) + 2 * j);
+                        float4 a = make_float4(acc[i][j].x, acc[i][j].y, acc[i][j + 1].x, acc[i][j + 1].y);
                         if (add) {
                             const float4 b = *o;
                             a = make_float4(b.x + a.x, b.y + a.y, b.z + a.z, b.w + a.w);
@@ -473,23 +516,29 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 }
 
 // dgamma (+)= the sum of the blocks' partial rows, in a fixed order: 32
-// columns per block, the rows dealt out to its 8 warps.
-__global__ void __launch_bounds__(256) dgamma_kernel(const float* __restrict__ partial, int parts, int cols,
-                                                     float* __restrict__ dgamma, int accumulate) {
-    __shared__ float sums[8][32];
+// columns per block, the rows dealt out to its 32 warps, whose loads are all in
+// flight together.
+constexpr int kDgammaWarps = 32;
+
+__global__ void __launch_bounds__(32 * kDgammaWarps) dgamma_kernel(const float* __restrict__ partial, int parts, int cols,
+                                                                   float* __restrict__ dgamma, int accumulate) {
+    __shared__ float sums[kDgammaWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
     griddep_launch_dependents();
     griddep_wait();
     float a = 0.0f;
-#pragma unroll 8
-    for (int p = warp; p < parts; p += 8) a += __ldcg(partial + static_cast<int64_t>(p) * cols + c);
+#pragma unroll 16
+    for (int p = warp; p < parts; p += kDgammaWarps) a += __ldcg(partial + static_cast<int64_t>(p) * cols + c);
     sums[warp][lane] = a;
     __syncthreads();
-    if (warp == 0) {
+    // warp w takes column w: its 32 sums by shuffles
+    a = sums[lane][warp];
 #pragma unroll
-        for (int w = 1; w < 8; ++w) a += sums[w][lane];
-        dgamma[c] = accumulate ? dgamma[c] + a : a;
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    if (lane == 0) {
+        float* out = dgamma + blockIdx.x * 32 + warp;
+        *out = accumulate ? *out + a : a;
     }
 }
 

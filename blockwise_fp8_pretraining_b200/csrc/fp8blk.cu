@@ -385,7 +385,8 @@ cudaError_t launch_norm_stream(const void* x, const void* residual, const void* 
     const int wpr = (chunks + 32 * CPL - 1) / (32 * CPL);
     const int teams = wpr < 8 ? 8 / wpr : 1;
     const int threads = 32 * wpr * teams;
-    const int64_t need = (rows + teams * R - 1) / (teams * R), cap = static_cast<int64_t>(sms) * (addnorm::kStreamThreads / threads);
+    const int64_t need = (rows + teams * R - 1) / (teams * R);
+    const int64_t cap = static_cast<int64_t>(sms) * (addnorm::kStreamThreads<CPL, R> * addnorm::kStreamBlocks<CPL, R> / threads);
     const int64_t each = (need + cap - 1) / cap;         // steps of the busiest block; the others' about as many
     return launch_pdl(addnorm::stream_kernel<CPL, R>, dim3(static_cast<unsigned>((need + each - 1) / each)),
                       dim3(static_cast<unsigned>(threads)), 0, stream, static_cast<const uint4*>(x),
@@ -413,16 +414,17 @@ fp8_status norm_rows(const void* x, const void* residual, const void* gamma, int
     const int chunks = static_cast<int>(cols / 8);
     cudaError_t e;
     // Few rows: a row over as many warps as it has 512-byte runs, so that a
-    // token's latency is one load and one short pass.  Many rows: 4 chunks per
-    // lane and step, of as few rows as that takes.
+    // token's latency is one load and one short pass.  Many rows: 2 chunks per
+    // lane and step, of two rows where one is enough for a row, and 4 where a row
+    // would not fit 12 warps otherwise.
     if (rows <= 2 * sms && chunks <= 1024)
         e = launch_norm_rows<1>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, s);
     else if (rows <= 2 * sms)
         e = launch_norm_rows<2>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, s);
     else if (chunks <= 32)
-        e = launch_norm_stream<1, 4>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, sms, s);
-    else if (chunks <= 64)
-        e = launch_norm_stream<2, 2>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, sms, s);
+        e = launch_norm_stream<1, 2>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, sms, s);
+    else if (chunks <= 768)
+        e = launch_norm_stream<2, 1>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, sms, s);
     else
         e = launch_norm_stream<4, 1>(x, residual, gamma, rows, chunks, eps, sum_out, rstd, q, s_row, sms, s);
     if (e != cudaSuccess) return cuda_fail("add + rmsnorm launch", e);
@@ -837,7 +839,7 @@ fp8_status fp8_rmsnorm_backward(const void* dy_bf16, const void* s_bf16, const f
     if (e != cudaSuccess) return cuda_fail("rmsnorm backward launch", e);
     if ((st = last_launch_status("rmsnorm backward launch")) != FP8_OK) return st;
     if (dgamma_f32 && b.grid > 1) {
-        e = launch_pdl(addnorm::dgamma_kernel, dim3(static_cast<unsigned>(cols / 32)), dim3(256), 0, s,
+        e = launch_pdl(addnorm::dgamma_kernel, dim3(static_cast<unsigned>(cols / 32)), dim3(32 * addnorm::kDgammaWarps), 0, s,
                        static_cast<const float*>(partial), static_cast<int>(b.grid), static_cast<int>(cols),
                        dgamma_f32, accumulate);
         if (e != cudaSuccess) return cuda_fail("dgamma launch", e);

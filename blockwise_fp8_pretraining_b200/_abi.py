@@ -293,58 +293,95 @@ def fp8_rmsnorm_quantize_1x128(x, rstd, gamma, mode=BOTH, q_row=None, s_row=None
     return outs
 
 
-def _alloc(shape, dtype, like, allocated):
-    # (from the cheapest call down: a small operator's time is mostly its outputs' allocation)
-    if dtype == like.dtype and shape == like.shape and like.is_contiguous():
-        t = torch.empty_like(like)
-    else:
-        t = like.new_empty(shape, dtype=dtype)
-    allocated.append(t)
+# The operators around the linears.  Their smallest calls take as long as the
+# host does, so a tensor is checked (device included) in one go, tensors made here
+# are not checked, and the messages are left to the checks above.
+
+def _on(t, dtype, shape, dev, name):
+    if t.get_device() == dev and t.dtype == dtype and t.shape == shape and t.is_contiguous():
+        return t
+    _want(t, dtype, shape, name)
+    _check_devices([(name, t)], dev)
     return t
 
 
-def _given(t, dtype, shape, like, allocated, name):
-    """t checked, or a new tensor noted in `allocated`."""
-    return _alloc(shape, dtype, like, allocated) if t is None else _want(t, dtype, shape, name)
+def _given(t, dtype, shape, like, dev, new, name):
+    """t checked, or a new tensor noted in `new` (from the cheapest call down)."""
+    if t is not None:
+        return _on(t, dtype, shape, dev, name)
+    if like.shape == shape and like.is_contiguous():
+        t = torch.empty_like(like) if like.dtype == dtype else torch.empty_like(like, dtype=dtype)
+    else:
+        t = like.new_empty(shape) if like.dtype == dtype else like.new_empty(shape, dtype=dtype)
+    new.append(t)
+    return t
+
+
+def _launch(dev, stream, new):
+    """The stream's handle, once the tensors' device is known to be current."""
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on cuda:{dev} but the current CUDA device is "
+                         f"cuda:{torch.cuda.current_device()}; call inside torch.cuda.device({dev})")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if not isinstance(stream, torch.cuda.Stream):      # a handle: scratch made here is the call's own to look after
+        stream = torch.cuda.ExternalStream(int(stream), device=dev)
+    _check_devices([], dev, stream)
+    _record(stream, new)
+    return stream.cuda_stream
+
+
+def _scratch(workspace, bytes_, like, dev, new):
+    """(pointer, bytes) of the workspace, allocated when left out."""
+    if workspace is None:
+        workspace = like.new_empty((bytes_(),), dtype=torch.uint8)
+        new.append(workspace)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
+        _check_devices([("workspace", workspace)], dev)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def fp8_add_rmsnorm_quantize_1x128(x, gamma, residual=None, eps=1e-6, mode=BOTH, sum_out=None, rstd=None, q_row=None,
                                    s_row=None, q_colT=None, s_col=None, stream=None):
     """s = bf16(x + residual) (s = x without a residual), RMSNorm of s with
-    the weight gamma, and its output quantized, in one pass.  Returns (s,
-    rstd, q_row, s_row, q_colT, s_col); entries of a grouping the mode leaves
-    out are None, and s is x itself without a residual.  sum_out may be x or
-    residual (in place)."""
-    lib = load()
-    if x.dtype != torch.bfloat16 or x.dim() != 2:
+    the weight gamma, and its output quantized.  Returns (s, rstd, q_row,
+    s_row, q_colT, s_col); entries of a grouping the mode leaves out are None,
+    and s is x itself without a residual.  sum_out may be x or residual (in
+    place)."""
+    lib = _lib or load()
+    bf16, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
+    if x.dtype != bf16 or x.dim() != 2:
         raise TypeError("x must be a 2-D bfloat16 tensor")
-    rows, cols = x.shape
-    _want(x, torch.bfloat16, (rows, cols), "x")
-    _want(gamma, torch.bfloat16, (cols,), "gamma")
+    shape = x.shape
+    rows, cols = shape
+    dev = x.get_device()
+    _on(x, bf16, shape, dev if dev >= 0 else None, "x")
+    _on(gamma, bf16, (cols,), dev, "gamma")
     new = []
     if residual is not None:
-        _want(residual, torch.bfloat16, (rows, cols), "residual")
-        sum_out = _given(sum_out, torch.bfloat16, (rows, cols), x, new, "sum_out")
+        _on(residual, bf16, shape, dev, "residual")
+        sum_out = _given(sum_out, bf16, shape, x, dev, new, "sum_out")
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual: without one the sum is x itself")
-    rstd = _given(rstd, torch.float32, (rows,), x, new, "rstd")
+    rstd = _given(rstd, f32, (rows,), x, dev, new, "rstd")
     if mode & ROWWISE:
-        q_row = _given(q_row, torch.uint8, (rows, cols), x, new, "q_row")
-        s_row = _given(s_row, torch.float32, (cols // 128, rows), x, new, "s_row")
+        q_row = _given(q_row, u8, shape, x, dev, new, "q_row")
+        s_row = _given(s_row, f32, (cols // 128, rows), rstd, dev, new, "s_row")
     else:
         q_row = s_row = None
     if mode & COLWISE:
-        q_colT = _given(q_colT, torch.uint8, (cols, rows), x, new, "q_colT")
-        s_col = _given(s_col, torch.float32, (rows // 128, cols), x, new, "s_col")
+        q_colT = _given(q_colT, u8, (cols, rows), x, dev, new, "q_colT")
+        s_col = _given(s_col, f32, (rows // 128, cols), rstd, dev, new, "s_col")
     else:
         q_colT = s_col = None
-    _launch_checks([("x", x), ("residual", residual), ("gamma", gamma), ("sum_out", sum_out), ("rstd", rstd),
-                    ("q_row", q_row), ("s_row", s_row), ("q_colT", q_colT), ("s_col", s_col)], stream)
-    _record(stream, new)
-    _check(lib.fp8_add_rmsnorm_quantize_1x128(_ptr(x), _ptr(residual), rows, cols, float(eps), _ptr(gamma), int(mode),
-                                              _ptr(sum_out), _ptr(rstd), _ptr(q_row), _ptr(s_row), _ptr(q_colT),
-                                              _ptr(s_col), _stream(stream)),
-           "fp8_add_rmsnorm_quantize_1x128")
+    handle = _launch(dev, stream, new)
+    st = lib.fp8_add_rmsnorm_quantize_1x128(x.data_ptr(), _ptr(residual), rows, cols, float(eps), gamma.data_ptr(),
+                                            int(mode), _ptr(sum_out), rstd.data_ptr(), _ptr(q_row), _ptr(s_row), _ptr(q_colT),
+                                            _ptr(s_col), handle)
+    if st:
+        raise Fp8Error(st, "fp8_add_rmsnorm_quantize_1x128")
     return (x if residual is None else sum_out), rstd, q_row, s_row, q_colT, s_col
 
 
@@ -364,29 +401,30 @@ def fp8_rmsnorm_backward(dy, s, rstd, gamma, dresidual=None, ds=None, dgamma=Non
     residual path's gradient of s if there is one.  ds (bf16) may be dy or
     dresidual (in place); dgamma is float32 [cols], added to with
     accumulate=True (it must then be given)."""
-    lib = load()
-    if s.dtype != torch.bfloat16 or s.dim() != 2:
+    lib = _lib or load()
+    bf16, f32 = torch.bfloat16, torch.float32
+    if s.dtype != bf16 or s.dim() != 2:
         raise TypeError("s must be a 2-D bfloat16 tensor")
-    rows, cols = s.shape
-    _want(s, torch.bfloat16, (rows, cols), "s")
-    _want(dy, torch.bfloat16, (rows, cols), "dy")
-    _want(rstd, torch.float32, (rows,), "rstd")
-    _want(gamma, torch.bfloat16, (cols,), "gamma")
+    shape = s.shape
+    rows, cols = shape
+    dev = s.get_device()
+    _on(s, bf16, shape, dev if dev >= 0 else None, "s")
+    _on(dy, bf16, shape, dev, "dy")
+    _on(rstd, f32, (rows,), dev, "rstd")
+    _on(gamma, bf16, (cols,), dev, "gamma")
     if dresidual is not None:
-        _want(dresidual, torch.bfloat16, (rows, cols), "dresidual")
+        _on(dresidual, bf16, shape, dev, "dresidual")
     if accumulate and dgamma is None:
         raise ValueError("accumulate=True needs the dgamma to add to")
     new = []
-    ds = _given(ds, torch.bfloat16, (rows, cols), s, new, "ds")
-    dgamma = _given(dgamma, torch.float32, (cols,), s, new, "dgamma")
-    _launch_checks([("dy", dy), ("s", s), ("rstd", rstd), ("gamma", gamma), ("dresidual", dresidual), ("ds", ds),
-                    ("dgamma", dgamma), ("workspace", workspace)], stream)
-    if workspace is None:
-        workspace = _alloc((fp8_rmsnorm_backward_workspace_bytes(rows, cols),), torch.uint8, s, new)
-    _record(stream, new)
-    _check(lib.fp8_rmsnorm_backward(_ptr(dy), _ptr(s), _ptr(rstd), _ptr(gamma), _ptr(dresidual), rows, cols, _ptr(ds),
-                                    _ptr(dgamma), int(bool(accumulate)), *_workspace(workspace), _stream(stream)),
-           "fp8_rmsnorm_backward")
+    ds = _given(ds, bf16, shape, s, dev, new, "ds")
+    dgamma = _given(dgamma, f32, (cols,), rstd, dev, new, "dgamma")
+    ws, size = _scratch(workspace, lambda: fp8_rmsnorm_backward_workspace_bytes(rows, cols), s, dev, new)
+    handle = _launch(dev, stream, new)
+    st = lib.fp8_rmsnorm_backward(dy.data_ptr(), s.data_ptr(), rstd.data_ptr(), gamma.data_ptr(), _ptr(dresidual), rows,
+                                  cols, ds.data_ptr(), dgamma.data_ptr(), 1 if accumulate else 0, ws, size, handle)
+    if st:
+        raise Fp8Error(st, "fp8_rmsnorm_backward")
     return ds, dgamma
 
 
@@ -396,17 +434,20 @@ _DTYPES = {torch.bfloat16: 0, torch.float32: 1}      # FP8_BF16, FP8_F32
 def _logits(t, name, like=None):
     """(dtype code, row stride) of a 2-D bf16 or float32 CUDA tensor whose
     rows are contiguous (a view into a padded vocabulary will do)."""
-    if t.dim() != 2 or t.dtype not in _DTYPES:
+    code = _DTYPES.get(t.dtype)
+    if code is None or t.dim() != 2:
         raise TypeError(f"{name} must be a 2-D bfloat16 or float32 tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if like is not None and (t.dtype != like.dtype or t.shape != like.shape):
         raise ValueError(f"{name}: expected {like.dtype} {tuple(like.shape)}, got {t.dtype} {tuple(t.shape)}")
     rows, vocab = t.shape
-    ld = t.stride(0) if rows > 1 else max(vocab, t.stride(0))
-    if (vocab > 1 and t.stride(1) != 1) or ld < vocab:
+    ld, one = t.stride()
+    if rows <= 1:
+        ld = max(vocab, ld)
+    if (vocab > 1 and one != 1) or ld < vocab:
         raise ValueError(f"{name}: rows must be contiguous and must not overlap")
-    return _DTYPES[t.dtype], ld
+    return code, ld
 
 
 def fp8_token_logprobs(logits, targets=None, topk=0, logprob=None, entropy=None, stats=None, top_logprob=None,
@@ -418,28 +459,29 @@ def fp8_token_logprobs(logits, targets=None, topk=0, logprob=None, entropy=None,
     by index) of bf16 or float32 logits [rows, vocab].  Returns (logprob,
     entropy, stats, top_logprob, top_index); logprob is None without targets,
     the last two with topk = 0."""
-    lib = load()
+    lib = _lib or load()
+    f32, i64 = torch.float32, torch.int64
     code, ld = _logits(logits, "logits")
     rows, vocab = logits.shape
+    dev = logits.get_device()
     new = []
+    entropy = _given(entropy, f32, (rows,), logits, dev, new, "entropy")
     if targets is not None:
-        _want(targets, torch.int64, (rows,), "targets")
-        logprob = _given(logprob, torch.float32, (rows,), logits, new, "logprob")
+        _on(targets, i64, (rows,), dev, "targets")
+        logprob = _given(logprob, f32, (rows,), entropy, dev, new, "logprob")
     else:
         logprob = None
-    entropy = _given(entropy, torch.float32, (rows,), logits, new, "entropy")
-    stats = _given(stats, torch.float32, (rows, 2), logits, new, "stats")
+    stats = _given(stats, f32, (rows, 2), entropy, dev, new, "stats")
     if topk:
-        top_logprob = _given(top_logprob, torch.float32, (rows, topk), logits, new, "top_logprob")
-        top_index = _given(top_index, torch.int64, (rows, topk), logits, new, "top_index")
+        top_logprob = _given(top_logprob, f32, (rows, topk), entropy, dev, new, "top_logprob")
+        top_index = _given(top_index, i64, (rows, topk), top_logprob, dev, new, "top_index")
     else:
         top_logprob = top_index = None
-    _launch_checks([("logits", logits), ("targets", targets), ("logprob", logprob), ("entropy", entropy),
-                    ("stats", stats), ("top_logprob", top_logprob), ("top_index", top_index)], stream)
-    _record(stream, new)
-    _check(lib.fp8_token_logprobs(_ptr(logits), code, rows, vocab, ld, _ptr(targets), int(topk), _ptr(logprob),
-                                  _ptr(entropy), _ptr(stats), _ptr(top_logprob), _ptr(top_index), _stream(stream)),
-           "fp8_token_logprobs")
+    handle = _launch(dev, stream, new)
+    st = lib.fp8_token_logprobs(logits.data_ptr(), code, rows, vocab, ld, _ptr(targets), int(topk), _ptr(logprob),
+                                entropy.data_ptr(), stats.data_ptr(), _ptr(top_logprob), _ptr(top_index), handle)
+    if st:
+        raise Fp8Error(st, "fp8_token_logprobs")
     return logprob, entropy, stats, top_logprob, top_index
 
 
@@ -448,32 +490,36 @@ def fp8_token_logprobs_backward(logits, targets, stats, dlogprob=None, entropy=N
     """Gradient of the logits from the gradients of fp8_token_logprobs's
     logprob and entropy (float32 [rows], either None); entropy is needed with
     dentropy.  dlogits (the logits' type) may be the logits themselves."""
-    lib = load()
+    lib = _lib or load()
+    f32 = torch.float32
     code, ld = _logits(logits, "logits")
     rows, vocab = logits.shape
-    _want(stats, torch.float32, (rows, 2), "stats")
+    dev = logits.get_device()
+    _on(stats, f32, (rows, 2), dev, "stats")
     if dlogprob is not None:
         if targets is None:
             raise ValueError("dlogprob needs targets")
-        _want(dlogprob, torch.float32, (rows,), "dlogprob")
+        _on(dlogprob, f32, (rows,), dev, "dlogprob")
     if targets is not None:
-        _want(targets, torch.int64, (rows,), "targets")
+        _on(targets, torch.int64, (rows,), dev, "targets")
     if dentropy is not None:
         if entropy is None:
             raise ValueError("dentropy needs the entropy")
-        _want(dentropy, torch.float32, (rows,), "dentropy")
-        _want(entropy, torch.float32, (rows,), "entropy")
+        _on(dentropy, f32, (rows,), dev, "dentropy")
+        _on(entropy, f32, (rows,), dev, "entropy")
     new = []
     if dlogits is None:
-        dlogits = _alloc((rows, vocab), logits.dtype, logits, new)
-    _, ld_out = _logits(dlogits, "dlogits", logits)
-    _launch_checks([("logits", logits), ("targets", targets), ("stats", stats), ("dlogprob", dlogprob),
-                    ("entropy", entropy), ("dentropy", dentropy), ("dlogits", dlogits)], stream)
-    _record(stream, new)
-    _check(lib.fp8_token_logprobs_backward(_ptr(logits), code, rows, vocab, ld, _ptr(targets), _ptr(stats),
-                                           _ptr(dlogprob), _ptr(entropy), _ptr(dentropy), _ptr(dlogits), ld_out,
-                                           _stream(stream)),
-           "fp8_token_logprobs_backward")
+        dlogits = _given(None, logits.dtype, (rows, vocab), logits, dev, new, "dlogits")
+        ld_out = vocab
+    else:
+        _, ld_out = _logits(dlogits, "dlogits", logits)
+        _check_devices([("dlogits", dlogits)], dev)
+    handle = _launch(dev, stream, new)
+    st = lib.fp8_token_logprobs_backward(logits.data_ptr(), code, rows, vocab, ld, _ptr(targets), stats.data_ptr(),
+                                         _ptr(dlogprob), _ptr(entropy), _ptr(dentropy), dlogits.data_ptr(), ld_out,
+                                         handle)
+    if st:
+        raise Fp8Error(st, "fp8_token_logprobs_backward")
     return dlogits
 
 
@@ -490,23 +536,23 @@ def fp8_newton_schulz(g, coefficients=NEWTON_SCHULZ_COEFFICIENTS, eps=1e-7, out=
     [batch, m, n], bf16 or float32), one step per (a, b, c) of coefficients.
     Returns a bf16 tensor of g's shape.  workspace: optional uint8 scratch of
     fp8_newton_schulz_workspace_bytes (allocated when left out)."""
-    lib = load()
+    lib = _lib or load()
     if g.dim() not in (2, 3) or g.dtype not in _DTYPES:
         raise TypeError("g must be a 2-D or 3-D bfloat16 or float32 tensor")
-    _want(g, g.dtype, g.shape, "g")
-    batch, m, n = g.shape if g.dim() == 3 else (1, *g.shape)
+    shape = g.shape
+    dev = g.get_device()
+    _on(g, g.dtype, shape, dev if dev >= 0 else None, "g")
+    batch, m, n = shape if g.dim() == 3 else (1, *shape)
     steps = len(coefficients)
     if any(len(step) != 3 for step in coefficients):
         raise ValueError("each step takes three coefficients")
     table = (ctypes.c_float * (3 * steps))(*[float(v) for step in coefficients for v in step])
     new = []
-    out = _given(out, torch.bfloat16, tuple(g.shape), g, new, "out")
-    _launch_checks([("g", g), ("out", out), ("workspace", workspace)], stream)
-    if workspace is None:
-        workspace = _alloc((fp8_newton_schulz_workspace_bytes(batch, m, n),), torch.uint8, g, new)
-    _record(stream, new)
-    _check(lib.fp8_newton_schulz(_ptr(g), _DTYPES[g.dtype], batch, m, n, ctypes.cast(table, ctypes.c_void_p), steps,
-                                 float(eps), _ptr(out), *_workspace(workspace), _stream(stream)),
+    out = _given(out, torch.bfloat16, shape, g, dev, new, "out")
+    ws, size = _scratch(workspace, lambda: fp8_newton_schulz_workspace_bytes(batch, m, n), g, dev, new)
+    handle = _launch(dev, stream, new)
+    _check(lib.fp8_newton_schulz(g.data_ptr(), _DTYPES[g.dtype], batch, m, n, ctypes.cast(table, ctypes.c_void_p),
+                                 steps, float(eps), out.data_ptr(), ws, size, handle),
            "fp8_newton_schulz")
     return out
 

@@ -543,7 +543,8 @@ struct NsLayout {
     int64_t s, l;               // shorter and longer side
     int64_t x_ld, s_ld;         // row strides of X and of S, Q (multiples of 64)
     bool tall;                  // more rows than columns
-    size_t partial, x[2], lo[2], gram, poly, bytes;   // X and what FP16 leaves of it, twice
+    size_t partial, x[2], lo[2], gram, poly, sums, flags, bytes;   // X and what FP16 leaves of it, twice
+    int slots;                  // partial sums of cut tiles
 };
 NsLayout ns_layout(int64_t batch, int64_t m, int64_t n) {
     NsLayout w;
@@ -561,7 +562,13 @@ NsLayout ns_layout(int64_t batch, int64_t m, int64_t n) {
     w.lo[1] = w.lo[0] + x;
     w.gram = w.lo[1] + x;
     w.poly = w.gram + q;
-    w.bytes = w.poly + q;
+    const int64_t side = (w.s + 255) / 256, symmetric = side * (side + 1) / 2 * batch;
+    const int64_t apply = side * ((w.l + 255) / 256) * batch, kb_s = (w.s + 63) / 64, kb_l = (w.l + 63) / 64;
+    w.slots = ns::slots_for(symmetric, kb_l);
+    if (ns::slots_for(apply, kb_s) > w.slots) w.slots = ns::slots_for(apply, kb_s);
+    w.sums = w.poly + q;
+    w.flags = w.sums + static_cast<size_t>(w.slots) * ns::kSlotFloat4 * sizeof(float4);
+    w.bytes = w.flags + up(static_cast<size_t>(w.slots) * 2 * ns::EPI_WARPS * sizeof(int));
     return w;
 }
 
@@ -589,7 +596,7 @@ std::atomic<int> g_ns_pairs[kMaxDevices][8];     // co-resident CTA pairs per ke
 
 template <int MODE, bool A_MN, bool B_MN>
 fp8_status launch_ns_gemm(int dev, int sms, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c,
-                          const CUtensorMap& t, ns::Params p, int64_t batch, cudaStream_t s) {
+                          const CUtensorMap& t, ns::Params p, int64_t batch, int slots, cudaStream_t s) {
     constexpr int variant = MODE * 2 + (MODE == ns::kGram ? A_MN : B_MN);
     auto kernel = ns::gemm_kernel<MODE, A_MN, B_MN>;
     if ((g_ns_attr_done[dev].load(std::memory_order_acquire) & (1 << variant)) == 0) {
@@ -608,12 +615,13 @@ fp8_status launch_ns_gemm(int dev, int sms, const CUtensorMap& a, const CUtensor
     }
     const int64_t total = static_cast<int64_t>(p.tiles) * batch;
     const int pairs = g_ns_pairs[dev][variant].load(std::memory_order_relaxed);
-    // Whole tiles for the full waves; the rest in halves when one wave of
-    // pairs can take all of them (a half tile takes about 3/4 of a whole one's
-    // time: its operands' traffic shrinks less than its products).
+    // Whole tiles for the full waves; the rest cut.
     const int64_t rest = total % pairs;
-    p.full = static_cast<int>(2 * rest <= pairs ? total - rest : total);
-    p.units = static_cast<int>(p.full + 2 * (total - p.full));
+    p.full = static_cast<int>(total - rest);
+    const ns::Cut cut = ns::best_cut(rest, pairs, (p.K + ns::BK - 1) / ns::BK, slots);
+    p.halves = cut.halves;
+    p.parts = cut.parts;
+    p.units = static_cast<int>(p.full + rest * cut.halves * cut.parts);
     const unsigned grid = 2u * static_cast<unsigned>(p.units < pairs ? p.units : pairs);
     const cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(ns::THREADS), ns::SMEM_BYTES, s, a, b, c, t, p);
     if (e != cudaSuccess) return cuda_fail("newton-schulz product launch", e);
@@ -622,7 +630,7 @@ fp8_status launch_ns_gemm(int dev, int sms, const CUtensorMap& a, const CUtensor
 
 template <typename T>
 fp8_status launch_ns_cast(const T* g, int64_t batch, int64_t m, int64_t n, int64_t ld, double* partial, float eps,
-                          float scale, __half* hi, __half* lo, int sms, cudaStream_t s) {
+                          float scale, __half* hi, __half* lo, int* flags, int num_flags, int sms, cudaStream_t s) {
     const bool vec = n * static_cast<int64_t>(sizeof(T)) % 16 == 0 && aligned16(g) && n % 8 == 0;
     const int64_t per_block = static_cast<int64_t>(ns::kNormThreads) * 16;
     int64_t parts = (m * n + per_block - 1) / per_block;
@@ -640,7 +648,7 @@ fp8_status launch_ns_cast(const T* g, int64_t batch, int64_t m, int64_t n, int64
     auto cast = vec ? ns::cast_kernel<T, true> : ns::cast_kernel<T, false>;
     e = launch_pdl(cast, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(batch)), block, 0, s, g,
                    static_cast<int>(m), static_cast<int>(n), static_cast<int>(ld), static_cast<const double*>(partial),
-                   static_cast<int>(parts), eps, scale, hi, lo);
+                   static_cast<int>(parts), eps, scale, hi, lo, flags, num_flags);
     if (e != cudaSuccess) return cuda_fail("newton-schulz cast launch", e);
     return last_launch_status("newton-schulz cast launch");
 }
@@ -931,10 +939,12 @@ fp8_status fp8_newton_schulz(const void* g, int dtype, int64_t batch, int64_t m,
     float scale = 1.0f;
     while (scale < 8192.0f && 4.0 * scale * scale <= static_cast<double>(m) * static_cast<double>(n)) scale *= 2.0f;
     double* partial = reinterpret_cast<double*>(ws + w.partial);
+    int* flags = reinterpret_cast<int*>(ws + w.flags);
+    const int num_flags = w.slots * 2 * ns::EPI_WARPS;
     st = dtype == FP8_F32 ? launch_ns_cast(static_cast<const float*>(g), batch, m, n, w.x_ld, partial, eps, scale, x[0],
-                                           lo[0], sms, s)
+                                           lo[0], flags, num_flags, sms, s)
                           : launch_ns_cast(static_cast<const __nv_bfloat16*>(g), batch, m, n, w.x_ld, partial, eps, scale,
-                                           x[0], lo[0], sms, s);
+                                           x[0], lo[0], flags, num_flags, sms, s);
     if (st != FP8_OK) return st;
 
     constexpr CUtensorMapSwizzle sw = CU_TENSOR_MAP_SWIZZLE_128B, flat = CU_TENSOR_MAP_SWIZZLE_NONE;
@@ -963,6 +973,8 @@ fp8_status fp8_newton_schulz(const void* g, int dtype, int64_t batch, int64_t m,
 
     ns::Params base{};
     base.wait_ns = g_wait_ns.load(std::memory_order_relaxed);
+    base.sums = reinterpret_cast<float4*>(ws + w.sums);
+    base.flags = flags;
     const int side = static_cast<int>((w.s + 255) / 256);
     for (int i = 0; i < steps; ++i) {
         const int cur = i & 1;
@@ -973,8 +985,11 @@ fp8_status fp8_newton_schulz(const void* g, int dtype, int64_t batch, int64_t m,
         p.tiles_m = p.tiles_n = side;
         p.tiles = side * (side + 1) / 2;
         p.alpha = 1.0f / (scale * scale);
-        st = w.tall ? launch_ns_gemm<ns::kGram, true, true>(dev, sms, x_half[cur], x_half[cur], s_out, s_outT, p, batch, s)
-                    : launch_ns_gemm<ns::kGram, false, false>(dev, sms, x_rows[cur], x_half[cur], s_out, s_outT, p, batch, s);
+        p.product = 3 * i + 1;
+        st = w.tall ? launch_ns_gemm<ns::kGram, true, true>(dev, sms, x_half[cur], x_half[cur], s_out, s_outT, p, batch,
+                                                            w.slots, s)
+                    : launch_ns_gemm<ns::kGram, false, false>(dev, sms, x_rows[cur], x_half[cur], s_out, s_outT, p, batch,
+                                                              w.slots, s);
         if (st != FP8_OK) return st;
         p.K = static_cast<int>(w.s);                         // Q
         p.a = lin ? 0.0f : coefficients[3 * i];
@@ -982,7 +997,8 @@ fp8_status fp8_newton_schulz(const void* g, int dtype, int64_t batch, int64_t m,
         p.c = coefficients[3 * i + 2];
         p.e0 = gram;
         p.e_ld = w.s_ld;
-        st = launch_ns_gemm<ns::kPoly, false, false>(dev, sms, s_in, s_half, q_out, q_outT, p, batch, s);
+        p.product = 3 * i + 2;
+        st = launch_ns_gemm<ns::kPoly, false, false>(dev, sms, s_in, s_half, q_out, q_outT, p, batch, w.slots, s);
         if (st != FP8_OK) return st;
         p = base;                                            // X
         p.M = static_cast<int>(m);
@@ -1003,8 +1019,11 @@ fp8_status fp8_newton_schulz(const void* g, int dtype, int64_t batch, int64_t m,
         p.carry = i < ns::kCarry && !p.final_out;
         p.out = p.final_out && !tma_out ? static_cast<__nv_bfloat16*>(out_bf16) : nullptr;
         const CUtensorMap& c = p.final_out ? final_map : x_out[cur ^ 1];
-        st = w.tall ? launch_ns_gemm<ns::kApply, false, false>(dev, sms, x_rows[cur], q_half, c, lo_out[cur ^ 1], p, batch, s)
-                    : launch_ns_gemm<ns::kApply, false, true>(dev, sms, q_in, x_half[cur], c, lo_out[cur ^ 1], p, batch, s);
+        p.product = 3 * i + 3;
+        st = w.tall ? launch_ns_gemm<ns::kApply, false, false>(dev, sms, x_rows[cur], q_half, c, lo_out[cur ^ 1], p, batch,
+                                                               w.slots, s)
+                    : launch_ns_gemm<ns::kApply, false, true>(dev, sms, q_in, x_half[cur], c, lo_out[cur ^ 1], p, batch,
+                                                              w.slots, s);
         if (st != FP8_OK) return st;
     }
     return FP8_OK;

@@ -29,14 +29,22 @@
 // 2 1.8e-3.)
 //
 // One GEMM kernel, C = A B^T in 256 x 256 tiles of CTA pairs, persistent:
-//   warp 0     operands by TMA into a ring of 64-deep stages
+//   warps 0, 2 operands by TMA into a ring of 64-deep stages, every other stage
+//              each (one thread needs about 260 clocks for a stage's barriers
+//              and 46 for each copy; a stage's products take 512)
 //   warp 1     tcgen05.mma.cta_group::2.kind::f16 into one of two 256-column
 //              TMEM accumulators (leader CTA)
 //   warps 4-11 epilogue: thread = one row, 128 columns; the other accumulator
 //              fills meanwhile
 // S and Q are symmetric: only tiles on or above the diagonal are computed, and
-// the epilogue stores each also transposed.  The tiles of a last, partly filled
-// wave are cut into two halves of 128 columns where the pairs suffice.
+// the epilogue stores each also transposed.
+//
+// The tiles of a last, partly filled wave are cut where there are pairs for the
+// pieces: into two halves of 128 columns, whose epilogues are half as long (their
+// products are not: a stage of 128 columns takes the same 512 clocks as one of
+// 256, because each commit holds up the next products' issue), and along the
+// contraction, where the parts before the last leave their FP32 sums in the
+// workspace and the pair with the last one adds them in order.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -70,7 +78,7 @@ static_assert(OFF_OUT % 1024 == 0, "swizzled staging must be 1024-byte aligned")
 
 constexpr int kMaxSide = 32768;
 constexpr int kCarry = 1;                  // steps whose X leaves as two FP16 numbers
-constexpr uint32_t kProducerSleepNs = 64;
+constexpr uint32_t kProducerSleepNs = 64, kEpilogueSleepNs = 128;
 
 enum Mode : int { kGram = 0, kPoly = 1, kApply = 2 };
 
@@ -78,8 +86,9 @@ struct Params {
     int M, N, K;                // output rows, output columns, contraction
     int tiles_m, tiles_n;       // 256 x 256 tiles
     int tiles;                  // per matrix (upper triangle for kGram, kPoly)
-    int full;                   // tiles (of all matrices) taken whole; the others as two halves
-    int units;                  // full + 2 * others
+    int full;                   // tiles (of all matrices) taken whole
+    int halves, parts;          // into which each tile behind those is cut: columns, contraction
+    int units;                  // full + halves * parts * others
     int row_fast;               // kApply: tiles of one column panel in a row (else of one row panel)
     float alpha;                // kGram: the accumulator's factor; kApply: the final output's
     float a, b, c;              // kPoly: Q = a I + b S + c S S; kApply: a of the linear term
@@ -89,8 +98,43 @@ struct Params {
     int carry;                  // kApply: also store what the FP16 rounding leaves of X (tmT)
     int final_out;              // kApply: bfloat16 output
     __nv_bfloat16* out;         // final output by plain stores (its rows not 16-byte multiples), else null
+    float4* sums;               // [slot][CTA][epilogue warp][4 chunks][8][lane]: partial sums
+    int* flags;                 // [slot][CTA][epilogue warp]: the product whose partial sums are there
+    int product;                // 1, 2, .. within a call
     uint64_t wait_ns;
 };
+
+constexpr int kMaxParts = 8;               // of one tile
+// What a tile costs besides its stages, in stages (0.3 us): the epilogue 6 us,
+// leaving partial sums 3 us, adding each 1 us.
+constexpr int kEpilogue = 20, kHandOver = 12, kAddPart = 4;
+constexpr int kSlots = 74;                 // partial sums at once, at most
+constexpr int kSlotFloat4 = 2 * EPI_WARPS * 4 * 8 * 32;
+
+// How `rest` tiles of num_kb stages are best cut for `pairs` pairs, with room
+// for `slots` partial sums.
+struct Cut {
+    int halves, parts;
+};
+inline Cut best_cut(int64_t rest, int pairs, int num_kb, int slots) {
+    Cut best = {1, 1};
+    int least = num_kb + kEpilogue;
+    for (int h = 1; h <= 2; ++h)
+        for (int c = 1; c <= kMaxParts && c <= num_kb && h * c * rest <= pairs && h * (c - 1) * rest <= slots; ++c) {
+            const int cost = (num_kb + c - 1) / c + (kEpilogue + (c > 1 ? kHandOver + kAddPart * (c - 1) : 0)) / h;
+            if (cost < least) {
+                best = {h, c};
+                least = cost;
+            }
+        }
+    return best;
+}
+// Partial sums a product of `tiles` tiles may leave, whatever the number of pairs.
+inline int slots_for(int64_t tiles, int64_t num_kb) {
+    if (num_kb <= kHandOver + kAddPart) return 0;       // (half of what is saved goes into handing over)
+    const int64_t most = 2 * tiles * (kMaxParts - 1);
+    return static_cast<int>(most < kSlots ? most : kSlots);
+}
 
 // 3-D tiled load into this CTA's shared memory, completing on a barrier of
 // either CTA of the pair.
@@ -139,23 +183,31 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool a_mn, bo
            (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// One unit of work: matrix z, output rows row0 .. + 255, columns col0 .. +
-// cols - 1 (256, or 128 for a half tile or where the matrix ends there).
-// diag: a tile on the diagonal, which is not mirrored.
+// One unit of work: output rows row0 .. + 255, columns col0 .. + cols - 1 (256,
+// or 128 for half a tile or where the matrix ends there) of matrix z, over
+// stages kb0 .. kb1 - 1 of the contraction.  diag: a tile on the diagonal, which
+// is not mirrored.  slot: the first partial sum of these columns.
 struct Unit {
-    int z, row0, col0, cols;
+    int z, row0, col0, cols, kb0, kb1, part, slot;
     bool diag;
 };
 
-// Unit u, or false where a half tile lies behind the matrix.
+// Unit u, or false where half a tile lies behind the matrix.
 template <int MODE>
-__device__ __forceinline__ bool unit_at(const Params& p, int u, Unit& w) {
+__device__ __forceinline__ bool unit_at(const Params& p, int num_kb, int u, Unit& w) {
     int tile = u, sub = 0;
     w.cols = BN;
+    w.part = w.slot = w.kb0 = 0;
+    w.kb1 = num_kb;
     if (u >= p.full) {
-        tile = p.full + ((u - p.full) >> 1);
-        sub = (u - p.full) & 1;
-        w.cols = BN / 2;
+        const int v = u - p.full, piece = v / p.parts;     // piece: columns of a tile
+        w.part = v - piece * p.parts;
+        w.slot = piece * (p.parts - 1);
+        w.kb0 = w.part * num_kb / p.parts;
+        w.kb1 = (w.part + 1) * num_kb / p.parts;
+        tile = p.full + piece / p.halves;
+        sub = piece % p.halves;
+        if (p.halves == 2) w.cols = BN / 2;
     }
     w.z = tile / p.tiles;
     int i = tile - w.z * p.tiles;
@@ -180,6 +232,38 @@ __device__ __forceinline__ bool unit_at(const Params& p, int u, Unit& w) {
     w.diag = tm == tn;
     if (p.N - w.col0 <= BN / 2) w.cols = BN / 2;
     return w.col0 < p.N;
+}
+
+__device__ __forceinline__ void st_release_flag(int* addr, int v) {
+    asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ int ld_acquire_flag(const int* addr) {
+    int v;
+    asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float2 half2_at(const uint4& v, int i) {
+    const uint32_t w = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+// Wait, no longer than limit_ns, until *flag is `want`.
+__device__ __forceinline__ bool flag_wait(const int* flag, int want, volatile int* abort, uint64_t limit_ns) {
+    uint64_t t0 = 0;
+    for (uint32_t it = 1; ld_acquire_flag(flag) != want; ++it) {
+        if ((it & 15u) != 0) continue;
+        if (*abort) return false;
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) {
+            t0 = now;
+        } else if (now - t0 > limit_ns) {
+            record_error(kErrTimeout);
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
 }
 
 // tmA, tmB: operands, [batch][rows][cols] FP16; box 64 x 128 for A, 64 x 64 for
@@ -238,79 +322,97 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     const uint32_t tmem_base = *reinterpret_cast<volatile uint32_t*>(smem + OFF_TMEM_SLOT);
     griddep_wait();                                      // inputs of the preceding kernel are complete
 
-    if (warp == 0) {
+    if (warp == 0 || warp == 2) {
         // -------------------------------------------------------- operands
         if (lane == 0) {
             const uint32_t full_leader = map_to_cta(full, 0);
-            int it = 0;
+            const int odd = warp >> 1;         // this warp's stages: the odd or the even ones of the block's sequence
+            int it = 0;                        // stages of the block so far
+            int st = odd, ph = 1;              // this warp's next stage in the ring, and its parity
+            int mine = 0;                      // stages this warp has requested
             bool ok = true;
             Unit w;
             for (int u = pair; ok && u < p.units; u += npairs) {
-                if (!unit_at<MODE>(p, u, w)) continue;
+                if (!unit_at<MODE>(p, num_kb, u, w)) continue;
                 const int m0 = w.row0 + static_cast<int>(rank) * BM;
                 const int n0 = w.col0 + static_cast<int>(rank) * (w.cols / 2);
+                const bool whole = w.cols == BN;
                 const uint32_t bytes = 2 * (A_BYTES + (w.cols / 2) * BK * 2);
-                for (int kb = 0; kb < num_kb; ++kb, ++it) {
-                    const int s = it % STAGES;
-                    if (!mbar_wait(empty + 8 * s, ((it / STAGES) & 1) ^ 1, abort_flag, p.wait_ns, kErrTimeout,
-                                   kProducerSleepNs)) {
+                for (int kb = w.kb0 + ((it ^ odd) & 1); kb < w.kb1; kb += 2) {
+                    if (!mbar_wait(empty + 8 * st, ph, abort_flag, p.wait_ns, kErrTimeout, kProducerSleepNs)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t dst = sbase + s * STAGE_BYTES, bar = full_leader + 8 * s;
-                    if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, bytes);
+                    const uint32_t dst = sbase + st * STAGE_BYTES, bar = full_leader + 8 * st;
+                    const int k = kb * BK;
+                    if (rank == 0) mbar_arrive_expect_tx(full + 8 * st, bytes);
                     if (A_MN) {
-                        tma_load_3d_pair(dst, &tmA, m0, kb * BK, w.z, bar);
-                        tma_load_3d_pair(dst + BOX_BYTES, &tmA, m0 + 64, kb * BK, w.z, bar);
+                        tma_load_3d_pair(dst, &tmA, m0, k, w.z, bar);
+                        tma_load_3d_pair(dst + BOX_BYTES, &tmA, m0 + 64, k, w.z, bar);
                     } else {
-                        tma_load_3d_pair(dst, &tmA, kb * BK, m0, w.z, bar);
+                        tma_load_3d_pair(dst, &tmA, k, m0, w.z, bar);
                     }
-                    for (int h = 0; h < w.cols / 128; ++h) {
-                        if (B_MN)
-                            tma_load_3d_pair(dst + A_BYTES + h * BOX_BYTES, &tmB, n0 + 64 * h, kb * BK, w.z, bar);
-                        else
-                            tma_load_3d_pair(dst + A_BYTES + h * BOX_BYTES, &tmB, kb * BK, n0 + 64 * h, w.z, bar);
+                    if (B_MN) {
+                        tma_load_3d_pair(dst + A_BYTES, &tmB, n0, k, w.z, bar);
+                        if (whole) tma_load_3d_pair(dst + A_BYTES + BOX_BYTES, &tmB, n0 + 64, k, w.z, bar);
+                    } else {
+                        tma_load_3d_pair(dst + A_BYTES, &tmB, k, n0, w.z, bar);
+                        if (whole) tma_load_3d_pair(dst + A_BYTES + BOX_BYTES, &tmB, k, n0 + 64, w.z, bar);
+                    }
+                    ++mine;
+                    if ((st += 2) >= STAGES) {
+                        st -= STAGES;
+                        ph ^= 1;
                     }
                 }
+                it += w.kb1 - w.kb0;
             }
             if (!ok && rank == 0) {
-                // let every copy already requested land (both CTAs' copies
-                // complete on the leader's barriers) before the pair exits
-                for (int j = max(0, it - STAGES); j < it; ++j) drain_wait(full + 8 * (j % STAGES), (j / STAGES) & 1, p.wait_ns);
+                // let every copy this warp has requested land (both CTAs'
+                // copies complete on the leader's barriers) before the pair exits
+                for (int j = max(0, mine - STAGES); j < mine; ++j) {
+                    const int i = 2 * j + odd;
+                    drain_wait(full + 8 * (i % STAGES), (i / STAGES) & 1, p.wait_ns);
+                }
             }
         }
         __syncwarp();
     } else if (warp == 1) {
         // ------------------------------------------------ MMA issuer (leader)
         if (lane == 0 && rank == 0) {
-            int it = 0, n = 0;
+            int n = 0, st = 0, ph = 0;
             bool ok = true;
             Unit w;
             for (int u = pair; ok && u < p.units; u += npairs) {
-                if (!unit_at<MODE>(p, u, w)) continue;
+                if (!unit_at<MODE>(p, num_kb, u, w)) continue;
                 const int buf = n & 1;
                 if (!mbar_wait(tempty + 8 * buf, ((n >> 1) & 1) ^ 1, abort_flag, p.wait_ns, kErrTimeout)) break;
                 ++n;
                 const uint32_t d_tmem = tmem_base + buf * BN;
                 const uint32_t idesc = w.cols == BN ? idesc_f16_f32(2 * BM, BN, A_MN, B_MN)
                                                     : idesc_f16_f32(2 * BM, BN / 2, A_MN, B_MN);
-                for (int kb = 0; kb < num_kb; ++kb, ++it) {
-                    const int s = it % STAGES;
-                    if (!mbar_wait(full + 8 * s, (it / STAGES) & 1, abort_flag, p.wait_ns, kErrTimeout)) {
+                bool ready = mbar_try_wait(full + 8 * st, ph);
+                for (int kb = w.kb0; kb < w.kb1; ++kb) {
+                    if (!ready && !mbar_wait(full + 8 * st, ph, abort_flag, p.wait_ns, kErrTimeout)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a_addr = sbase + s * STAGE_BYTES;
+                    const uint32_t a_addr = sbase + st * STAGE_BYTES, done = empty + 8 * st;
                     const uint64_t a_desc = A_MN ? smem_desc_mn64_sw128(a_addr) : smem_desc_k128_sw128(a_addr);
                     const uint64_t b_desc =
                         B_MN ? smem_desc_mn64_sw128(a_addr + A_BYTES) : smem_desc_k128_sw128(a_addr + A_BYTES);
+                    if (++st == STAGES) {
+                        st = 0;
+                        ph ^= 1;
+                    }
                     // 16 of the contraction: 32 bytes along a swizzled row, or 16 rows of 128 bytes
                     constexpr uint64_t adv_a = (A_MN ? 16 * 128 : 32) >> 4, adv_b = (B_MN ? 16 * 128 : 32) >> 4;
 #pragma unroll
                     for (int k = 0; k < BK / 16; ++k)
-                        mma_f16_pair(d_tmem, a_desc + k * adv_a, b_desc + k * adv_b, idesc, (kb | k) != 0 ? 1u : 0u);
-                    mma_commit_pair(empty + 8 * s, 0x3);
+                        mma_f16_pair(d_tmem, a_desc + k * adv_a, b_desc + k * adv_b, idesc, (kb > w.kb0 || k > 0) ? 1u : 0u);
+                    mma_commit_pair(done, 0x3);
+                    ready = kb + 1 < w.kb1 && mbar_try_wait(full + 8 * st, ph);    // (asked while these products run)
                 }
                 if (ok) mma_commit_pair(tfull + 8 * buf, 0x3);
             }
@@ -333,12 +435,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
         int n = 0;
         Unit w;
         for (int u = pair; u < p.units; u += npairs) {
-            if (!unit_at<MODE>(p, u, w)) continue;
+            if (!unit_at<MODE>(p, num_kb, u, w)) continue;
             const int buf = n & 1;
             const int row0 = w.row0 + static_cast<int>(rank) * BM + quarter * 32;
             const int row = row0 + lane;
-            const int chunks = w.cols / 64;        // of 32 columns, per half
             const int cbase = w.col0 + half * (w.cols / 2);
+            const int chunks = min(w.cols / 64, 2 * ((max(p.N - cbase, 0) + 63) / 64));      // of 32 columns: whole boxes
+            const bool last_part = u < p.full || w.part == p.parts - 1;
+            const int others = w.part;             // partial sums to add
+            // this warp's piece of partial sum `part`
+            auto sums = [&](int part) {
+                return p.sums + (static_cast<int64_t>(w.slot + part) * 2 * EPI_WARPS + rank * EPI_WARPS + ew) * (4 * 8 * 32) + lane;
+            };
+            auto flag = [&](int part) { return p.flags + (w.slot + part) * 2 * EPI_WARPS + rank * EPI_WARPS + ew; };
             // S, or X's two parts, of the row's 32 columns from c on
             uint4 e[NE];
             auto fetch = [&](int c) {
@@ -351,61 +460,95 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     e[j] = in ? __ldg(reinterpret_cast<const uint4*>(src + at) + (j & 3)) : make_uint4(0u, 0u, 0u, 0u);
                 }
             };
-            fetch(cbase);
-            const bool got = mbar_wait(tfull + 8 * buf, (n >> 1) & 1, abort_flag, p.wait_ns, kErrTimeout);
+            if (last_part) fetch(cbase);
+            bool got = mbar_wait(tfull + 8 * buf, (n >> 1) & 1, abort_flag, p.wait_ns, kErrTimeout, kEpilogueSleepNs);
             if (!__all_sync(0xffffffffu, got)) break;
             ++n;
             tc_fence_after();
+            if (last_part && others > 0) {
+                if (lane < others) got = flag_wait(flag(lane), p.product, abort_flag, p.wait_ns);
+                if (!__all_sync(0xffffffffu, got)) break;
+            }
+            auto release = [&] {                   // the accumulator may be refilled
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (rank == 0)
+                        mbar_arrive(tempty + 8 * buf);
+                    else
+                        mbar_arrive_remote(tempty_leader + 8 * buf);
+                }
+            };
+            if (chunks == 0) release();
 #pragma unroll 1
             for (int ch = 0; ch < chunks; ++ch) {
                 const int col = cbase + 32 * ch;
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(lane_base + buf * BN + half * (w.cols / 2) + 32 * ch, r);
                 tmem_ld_wait();
-                if (ch == chunks - 1) {            // the accumulator may be refilled
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (rank == 0)
-                            mbar_arrive(tempty + 8 * buf);
-                        else
-                            mbar_arrive_remote(tempty_leader + 8 * buf);
+                if (ch == chunks - 1) release();
+                if (!last_part) {
+                    float4* dst = sums(w.part) + ch * (8 * 32);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        __stcg(dst + j * 32, make_float4(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1]),
+                                                         __uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])));
+                    continue;
+                }
+                for (int q = 0; q < others; ++q) {
+                    const float4* src = sums(q) + ch * (8 * 32);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float4 v = __ldcg(src + j * 32);
+                        r[4 * j] = __float_as_uint(__uint_as_float(r[4 * j]) + v.x);
+                        r[4 * j + 1] = __float_as_uint(__uint_as_float(r[4 * j + 1]) + v.y);
+                        r[4 * j + 2] = __float_as_uint(__uint_as_float(r[4 * j + 2]) + v.z);
+                        r[4 * j + 3] = __float_as_uint(__uint_as_float(r[4 * j + 3]) + v.w);
                     }
                 }
-                uint32_t o[16], lo[16];            // the row's 32 results, two per word
+                // (branches outside the loops: inside them each costs the epilogue more than the arithmetic)
+                float2 v[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    float v0 = __uint_as_float(r[2 * j]), v1 = __uint_as_float(r[2 * j + 1]);
-                    if (MODE == kGram) {
-                        v0 *= p.alpha;
-                        v1 *= p.alpha;
+                    v[j] = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                    if (MODE == kGram) v[j] = __fmul2_rn(v[j], make_float2(p.alpha, p.alpha));
+                    if (MODE == kPoly)
+                        v[j] = __ffma2_rn(make_float2(p.c, p.c), v[j],
+                                          __fmul2_rn(make_float2(p.b, p.b), half2_at(e[(j >> 2) % NE], j & 3)));
+                }
+                if (MODE == kPoly && row0 == col) {                        // a I: each lane's own column
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        v[j].x += lane == 2 * j ? p.a : 0.0f;
+                        v[j].y += lane == 2 * j + 1 ? p.a : 0.0f;
                     }
-                    if (MODE == kPoly) {
-                        const uint32_t sw = reinterpret_cast<const uint32_t*>(&e[j >> 2])[j & 3];
-                        const float2 s2 = __half22float2(*reinterpret_cast<const __half2*>(&sw));
-                        v0 = fmaf(p.c, v0, p.b * s2.x) + (row == col + 2 * j && row < p.M ? p.a : 0.0f);
-                        v1 = fmaf(p.c, v1, p.b * s2.y) + (row == col + 2 * j + 1 && row < p.M ? p.a : 0.0f);
+                }
+                if (lin) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        v[j] = __ffma2_rn(make_float2(p.a, p.a),
+                                          __fadd2_rn(half2_at(e[(j >> 2) % NE], j & 3), half2_at(e[(4 + (j >> 2)) % NE], j & 3)),
+                                          v[j]);
+                }
+                uint32_t o[16], lo[16];            // the row's 32 results, two per word
+                if (MODE == kApply && p.final_out) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[j].x * p.alpha, v[j].y * p.alpha);
+                        o[j] = *reinterpret_cast<const uint32_t*>(&b2);
                     }
-                    if (MODE == kApply) {
-                        if (lin) {
-                            const uint32_t hw = reinterpret_cast<const uint32_t*>(&e[(j >> 2) % NE])[j & 3];
-                            const uint32_t lw = reinterpret_cast<const uint32_t*>(&e[(4 + (j >> 2)) % NE])[j & 3];
-                            const float2 h2 = __half22float2(*reinterpret_cast<const __half2*>(&hw));
-                            const float2 l2 = __half22float2(*reinterpret_cast<const __half2*>(&lw));
-                            v0 = fmaf(p.a, h2.x + l2.x, v0);
-                            v1 = fmaf(p.a, h2.y + l2.y, v1);
-                        }
-                        if (p.final_out) {
-                            const __nv_bfloat162 b2 = __floats2bfloat162_rn(v0 * p.alpha, v1 * p.alpha);
-                            o[j] = *reinterpret_cast<const uint32_t*>(&b2);
-                            continue;
-                        }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const __half2 h2 = __floats2half2_rn(v[j].x, v[j].y);
+                        o[j] = *reinterpret_cast<const uint32_t*>(&h2);
                     }
-                    const __half2 h2 = __floats2half2_rn(v0, v1);
-                    o[j] = *reinterpret_cast<const uint32_t*>(&h2);
-                    if (MODE == kApply && p.carry) {
-                        const float2 back = __half22float2(h2);
-                        const __half2 l2 = __floats2half2_rn(v0 - back.x, v1 - back.y);
+                }
+                if (MODE == kApply && p.carry) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&o[j]));
+                        const __half2 l2 = __floats2half2_rn(v[j].x - back.x, v[j].y - back.y);
                         lo[j] = *reinterpret_cast<const uint32_t*>(&l2);
                     }
                 }
@@ -465,6 +608,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
                     }
                 }
             }
+            if (!last_part) {
+                __syncwarp();
+                if (lane == 0) st_release_flag(flag(w.part), p.product);
+            }
         }
         if (lane == 0) bulk_wait_group0();                 // output stores complete
         __syncwarp();
@@ -481,7 +628,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
 // --------------------------------------------------- Frobenius norm and cast
 
-constexpr int kNormBlocks = 256;            // at most, per matrix
+constexpr int kNormBlocks = 1024;           // at most, per matrix
 constexpr int kNormThreads = 256;
 
 __device__ __forceinline__ double block_sum(double v, double* red) {
@@ -539,12 +686,17 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const T* __restrict_
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kNormThreads)
     cast_kernel(const T* __restrict__ g, int rows, int n, int ld, const double* __restrict__ partial, int parts,
-                float eps, float scale, __half* __restrict__ hi, __half* __restrict__ lo) {
+                float eps, float scale, __half* __restrict__ hi, __half* __restrict__ lo, int* __restrict__ flags,
+                int num_flags) {
     __shared__ double red[kNormThreads / 32];
     griddep_launch_dependents();
     griddep_wait();
     const int64_t z = blockIdx.y;
-    const double norm = sqrt(block_sum(static_cast<int>(threadIdx.x) < parts ? partial[z * parts + threadIdx.x] : 0.0, red)) +
+    if (blockIdx.x == 0 && z == 0)         // no product's partial sums are there yet
+        for (int i = threadIdx.x; i < num_flags; i += kNormThreads) flags[i] = 0;
+    double mine = 0.0;
+    for (int i = threadIdx.x; i < parts; i += kNormThreads) mine += partial[z * parts + i];
+    const double norm = sqrt(block_sum(mine, red)) +
                         static_cast<double>(eps);
     double f = norm > 0.0 ? static_cast<double>(scale) / norm : norm == norm ? 0.0 : norm;
     float p1 = 1.0f, p2 = 1.0f, fr;

@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
     __shared__ float4 parts[kWarps];
     __shared__ float4 block_part;
     __shared__ uint32_t bound[kWarps];
-    __shared__ __align__(16) uint32_t posts[TOPK ? kTeams : 1][kPosts];
+    __shared__ __align__(16) uint32_t posts[TOPK ? kPosts : 4];
     __shared__ __align__(16) uint64_t cand[TOPK ? kWarps * 32 : 1];     // kTeams * 32 at least
     __shared__ uint64_t best[TOPK ? kTeams : 1][32];
     __shared__ int count[kTeams];
@@ -429,35 +429,39 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
         if (TOPK) {
             const uint32_t bo = i0 < nvec && bm == bm ? order_of(bm) : 0u;
             if (first) {
-                // The lanes' maxima are distinct elements.  Each warp's `r` largest are
-                // posted, 2 topk of the block or more (all of them where a warp has no
-                // more), and the topk-th largest of those is a bound.
-                const int r = min(32, (2 * topk + nw - 1) / nw);
+                // The lanes' maxima are distinct elements: the topk-th largest of some of
+                // them is a bound.  One warp takes it from all of its own; several post
+                // their `r` largest each, 2 topk of the block or more.
                 int above = 0;
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
                     const uint32_t o = __shfl_sync(0xffffffffu, bo, j);
                     above += (o > bo || (o == bo && j < lane)) ? 1 : 0;
                 }
-                if (above < r) posts[team][warp * r + above] = bo;
-                sync();
-                const int posted = nw * r;     // at most 79
-                uint32_t mine[3], cut = 0;
-                int reached[3] = {0, 0, 0};
+                uint32_t cut = above == topk - 1 ? bo : 0u;
+                if (nw > 1) {
+                    cut = 0;
+                    const int r = (2 * topk + nw - 1) / nw;
+                    if (above < r) posts[warp * r + above] = bo;
+                    __syncthreads();
+                    const int posted = nw * r;     // at most 79
+                    uint32_t mine[3];
+                    int reached[3] = {0, 0, 0};
 #pragma unroll
-                for (int i = 0; i < 3; ++i) mine[i] = lane + 32 * i < posted ? posts[team][lane + 32 * i] : 0u;
-                for (int j = 0; j < posted; j += 4) {
-                    uint4 q = *reinterpret_cast<const uint4*>(&posts[team][j]);
-                    q.y = j + 1 < posted ? q.y : 0u;
-                    q.z = j + 2 < posted ? q.z : 0u;
-                    q.w = j + 3 < posted ? q.w : 0u;
+                    for (int i = 0; i < 3; ++i) mine[i] = lane + 32 * i < posted ? posts[lane + 32 * i] : 0u;
+                    for (int j = 0; j < posted; j += 4) {
+                        uint4 q = *reinterpret_cast<const uint4*>(&posts[j]);
+                        q.y = j + 1 < posted ? q.y : 0u;
+                        q.z = j + 2 < posted ? q.z : 0u;
+                        q.w = j + 3 < posted ? q.w : 0u;
+#pragma unroll
+                        for (int i = 0; i < 3; ++i)
+                            reached[i] += (q.x >= mine[i]) + (q.y >= mine[i]) + (q.z >= mine[i]) + (q.w >= mine[i]);
+                    }
 #pragma unroll
                     for (int i = 0; i < 3; ++i)
-                        reached[i] += (q.x >= mine[i]) + (q.y >= mine[i]) + (q.z >= mine[i]) + (q.w >= mine[i]);
+                        if (reached[i] >= topk) cut = max(cut, mine[i]);
                 }
-#pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    if (reached[i] >= topk) cut = max(cut, mine[i]);
                 reach0 = __reduce_max_sync(0xffffffffu, cut);
             }
             uint32_t reach = max(reach0, __reduce_min_sync(0xffffffffu, bounds[lane & (nw - 1)]));

@@ -484,12 +484,13 @@ bool element_aligned(const void* p, int dtype) {
 }
 
 // A row of logits over `ranks` CTAs.  Few rows are split as long as every CTA
-// can be resident at once and has 16 KB of the row.  An SM holds 1024 threads:
-// blocks are made small enough for all rows to be resident together where that
-// is possible (a second, mostly empty wave would double the time), and large
-// where there are many waves anyway (fewer rows at once, less left over at the
-// end).  A thread has at least one batch of 16-byte vectors; rows of one warp
-// share a block.
+// can be resident at once and has 16 KB of the row.  The more rows there are, the
+// smaller their blocks: more rows are then under way at once, whose beginnings and
+// ends hide behind one another ([4096, 151936] bf16 took 225 us in blocks of 512
+// threads, 198 of 256, 195 of 128, 197 of 64, and with 20 alternatives 417, 343,
+// 304 and 302; [600, 151936] 43, 42 and, of 128, 60).  A thread has at least one
+// batch of 16-byte vectors, and four where rows abound; rows of one warp share a
+// block.
 template <typename T>
 fp8_status launch_logp(const void* logits, int64_t rows, int64_t vocab, int64_t ld, const int64_t* targets, int topk,
                        float* logprob, float* entropy, float* stats, float* top_logprob, int64_t* top_index,
@@ -502,8 +503,9 @@ fp8_status launch_logp(const void* logits, int64_t rows, int64_t vocab, int64_t 
     int ranks = 1;
     while (ranks < logp::kMaxRanks && rows * ranks <= sms && bytes / (2 * ranks) >= 16384) ranks *= 2;
     const int64_t ctas = rows * ranks;
-    const int most = ctas <= 2 * sms || ctas > 8 * sms ? logp::kMaxThreads : ctas <= 4 * sms ? 256 : 128;
-    const int threads = pow2_between(bytes / ranks / (16 * logp::kBatch), 32, most);
+    const int most = ctas <= 3 * sms ? logp::kMaxThreads : ctas <= 8 * sms ? 256 : ctas <= 16 * sms ? 128 : 64;
+    const int batches = ctas > 32 * static_cast<int64_t>(sms) ? 4 : 1;
+    const int threads = pow2_between(bytes / ranks / (16 * logp::kBatch * batches), 32, most);
     const int warps = threads / 32, teams = warps == 1 ? logp::kTeams : 1;
     const int64_t grid = (ctas + teams - 1) / teams;
     if (grid > kMaxDim) return FP8_ERR_SHAPE;

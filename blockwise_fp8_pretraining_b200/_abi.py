@@ -1,4 +1,6 @@
 """ctypes binding of the C ABI in include/fp8blk.h (argument marshalling only).
+The operators whose smallest calls last as long as their marshalling have it
+compiled as well (csrc/host.cpp), for plain calls on the current stream.
 
 Every function here has the name of the C entry point it calls.  Tensors are
 torch CUDA tensors; outputs the caller does not pass are allocated with torch
@@ -9,6 +11,8 @@ blockwise_fp8_pretraining_b200.build``); there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import re
 
@@ -25,6 +29,7 @@ MAX_TOPK = 32                          # FP8_MAX_TOPK
 NEWTON_SCHULZ_COEFFICIENTS = ((3.4445, -4.7750, 2.0315),) * 5
 
 _lib = None
+_host = None                           # the compiled host side, where it was built for this torch
 
 
 class Fp8Error(RuntimeError):
@@ -98,8 +103,31 @@ def load() -> ctypes.CDLL:
     lib.fp8_status_string.restype = ctypes.c_char_p
     lib.fp8_last_cuda_error.argtypes = []
     lib.fp8_last_cuda_error.restype = ctypes.c_char_p
+    _load_host(lib)
     _lib = lib
     return lib
+
+
+def _load_host(lib) -> None:
+    global _host
+    if not os.path.exists(_build.HOST_LIB):
+        return
+    loader = importlib.machinery.ExtensionFileLoader("_fp8blk_host", _build.HOST_LIB)
+    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fp8blk_host", loader))
+    loader.exec_module(module)
+    module.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
+        lib.fp8_add_rmsnorm_quantize_1x128, lib.fp8_rmsnorm_backward, lib.fp8_rmsnorm_backward_workspace_bytes,
+        lib.fp8_token_logprobs, lib.fp8_token_logprobs_backward)))
+    _host = module
+
+
+def _plain(function: str, where: str, *args):
+    """The compiled host side's result, or None where the call is not plain
+    (see csrc/host.cpp) and goes through the checks below."""
+    out = getattr(_host, function)(*args)
+    if type(out) is int:
+        raise Fp8Error(out, where)
+    return out
 
 
 def status_string(status: int) -> str:
@@ -351,6 +379,11 @@ def fp8_add_rmsnorm_quantize_1x128(x, gamma, residual=None, eps=1e-6, mode=BOTH,
     and s is x itself without a residual.  sum_out may be x or residual (in
     place)."""
     lib = _lib or load()
+    if stream is None and _host is not None:
+        out = _plain("add_rmsnorm_quantize", "fp8_add_rmsnorm_quantize_1x128", x, gamma, residual, eps, mode, sum_out, rstd,
+                     q_row, s_row, q_colT, s_col)
+        if out is not None:
+            return out
     bf16, f32, u8 = torch.bfloat16, torch.float32, torch.uint8
     if x.dtype != bf16 or x.dim() != 2:
         raise TypeError("x must be a 2-D bfloat16 tensor")
@@ -402,6 +435,11 @@ def fp8_rmsnorm_backward(dy, s, rstd, gamma, dresidual=None, ds=None, dgamma=Non
     dresidual (in place); dgamma is float32 [cols], added to with
     accumulate=True (it must then be given)."""
     lib = _lib or load()
+    if stream is None and _host is not None:
+        out = _plain("rmsnorm_backward", "fp8_rmsnorm_backward", dy, s, rstd, gamma, dresidual, ds, dgamma, accumulate,
+                     workspace)
+        if out is not None:
+            return out
     bf16, f32 = torch.bfloat16, torch.float32
     if s.dtype != bf16 or s.dim() != 2:
         raise TypeError("s must be a 2-D bfloat16 tensor")
@@ -460,6 +498,11 @@ def fp8_token_logprobs(logits, targets=None, topk=0, logprob=None, entropy=None,
     entropy, stats, top_logprob, top_index); logprob is None without targets,
     the last two with topk = 0."""
     lib = _lib or load()
+    if stream is None and _host is not None:
+        out = _plain("token_logprobs", "fp8_token_logprobs", logits, targets, topk, logprob, entropy, stats, top_logprob,
+                     top_index)
+        if out is not None:
+            return out
     f32, i64 = torch.float32, torch.int64
     code, ld = _logits(logits, "logits")
     rows, vocab = logits.shape
@@ -472,7 +515,7 @@ def fp8_token_logprobs(logits, targets=None, topk=0, logprob=None, entropy=None,
     else:
         logprob = None
     stats = _given(stats, f32, (rows, 2), entropy, dev, new, "stats")
-    if topk:
+    if topk > 0:
         top_logprob = _given(top_logprob, f32, (rows, topk), entropy, dev, new, "top_logprob")
         top_index = _given(top_index, i64, (rows, topk), top_logprob, dev, new, "top_index")
     else:
@@ -491,6 +534,11 @@ def fp8_token_logprobs_backward(logits, targets, stats, dlogprob=None, entropy=N
     logprob and entropy (float32 [rows], either None); entropy is needed with
     dentropy.  dlogits (the logits' type) may be the logits themselves."""
     lib = _lib or load()
+    if stream is None and _host is not None:
+        out = _plain("token_logprobs_backward", "fp8_token_logprobs_backward", logits, targets, stats, dlogprob, entropy,
+                     dentropy, dlogits)
+        if out is not None:
+            return out
     f32 = torch.float32
     code, ld = _logits(logits, "logits")
     rows, vocab = logits.shape

@@ -387,8 +387,7 @@ cudaError_t launch_norm_stream(const void* x, const void* residual, const void* 
     const int threads = 32 * wpr * teams;
     const int64_t need = (rows + teams * R - 1) / (teams * R);
     const int64_t cap = static_cast<int64_t>(sms) * (addnorm::kStreamThreads<CPL, R> * addnorm::kStreamBlocks<CPL, R> / threads);
-    const int64_t each = (need + cap - 1) / cap;         // steps of the busiest block; the others' about as many
-    return launch_pdl(addnorm::stream_kernel<CPL, R>, dim3(static_cast<unsigned>((need + each - 1) / each)),
+    return launch_pdl(addnorm::stream_kernel<CPL, R>, dim3(static_cast<unsigned>(need < cap ? need : cap)),
                       dim3(static_cast<unsigned>(threads)), 0, stream, static_cast<const uint4*>(x),
                       static_cast<const uint4*>(residual), static_cast<const uint4*>(gamma), rows, chunks, eps, wpr,
                       static_cast<uint4*>(sum_out), rstd, reinterpret_cast<uint2*>(q), s_row);

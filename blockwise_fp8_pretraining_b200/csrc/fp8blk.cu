@@ -502,7 +502,7 @@ fp8_status launch_logp(const void* logits, int64_t rows, int64_t vocab, int64_t 
     int ranks = 1;
     while (ranks < logp::kMaxRanks && rows * ranks <= sms && bytes / (2 * ranks) >= 16384) ranks *= 2;
     const int64_t ctas = rows * ranks;
-    const int most = ctas <= 3 * sms ? logp::kMaxThreads : ctas <= 8 * sms ? 256 : ctas <= 16 * sms ? 128 : 64;
+    const int most = ctas <= 3 * sms ? logp::kMaxThreads : ctas <= 7 * sms ? 256 : ctas <= 16 * sms ? 128 : 64;
     const int batches = ctas > 32 * static_cast<int64_t>(sms) ? 4 : 1;
     const int threads = pow2_between(bytes / ranks / (16 * logp::kBatch * batches), 32, most);
     const int warps = threads / 32, teams = warps == 1 ? logp::kTeams : 1;

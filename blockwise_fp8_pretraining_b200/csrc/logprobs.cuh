@@ -255,26 +255,45 @@ __device__ __forceinline__ uint64_t key_of(float x, int64_t index) {
 // The warp's list: lane i holds the i-th largest key (0: none).
 struct TopList {
     uint64_t key;
-    __device__ __forceinline__ void insert(uint64_t k, int lane) {
-        const int pos = __popc(__ballot_sync(0xffffffffu, key > k));
-        const uint64_t up = __shfl_up_sync(0xffffffffu, key, 1);
-        key = lane < pos ? key : lane == pos ? k : up;
-    }
-    // every lane offers one key (0: none) that beats the list's entry `at`
+    // every lane offers one key (0: none); `at`: the last entry that matters
     __device__ __forceinline__ void offer(uint64_t k, int at, int lane) {
-        uint64_t worst = __shfl_sync(0xffffffffu, key, at);
-        uint32_t left = __ballot_sync(0xffffffffu, k > worst);
-        while (left) {
+        uint32_t left = __ballot_sync(0xffffffffu, k > __shfl_sync(0xffffffffu, key, at));
+        while (left) {                     // (a key that no longer belongs finds no place)
             const int src = __ffs(left) - 1;
             left &= left - 1;
             const uint64_t c = __shfl_sync(0xffffffffu, k, src);
-            if (c > worst) {
-                insert(c, lane);
-                worst = __shfl_sync(0xffffffffu, key, at);
-            }
+            const uint64_t up = __shfl_up_sync(0xffffffffu, key, 1);
+            const int pos = __popc(__ballot_sync(0xffffffffu, key > c));
+            key = lane < pos ? key : lane == pos ? c : up;
         }
     }
+    __device__ __forceinline__ uint32_t order() const { return static_cast<uint32_t>(key >> 32); }
 };
+
+// A bound that topk elements of the block reach: the topk-th largest of what
+// its warps post, r values each in descending order (lane i < r: the i-th).  Each
+// warp counts for its own values how many of all reach them.  *cut starts at 0.
+__device__ __forceinline__ uint32_t block_bound(uint32_t* posts, uint32_t* cut, uint32_t value, int r, int nw, int topk,
+                                                int warp, int lane) {
+    if (lane < r) posts[warp * r + lane] = value;
+    __syncthreads();
+    const int posted = nw * r;             // at most 79
+    const uint32_t p0 = lane < posted ? posts[lane] : 0u, p1 = lane + 32 < posted ? posts[lane + 32] : 0u,
+                   p2 = lane + 64 < posted ? posts[lane + 64] : 0u;
+    for (int i = 0; i < r; ++i) {
+        const uint32_t v = __shfl_sync(0xffffffffu, value, i);
+        if (v == 0) break;
+        int reached = __popc(__ballot_sync(0xffffffffu, p0 >= v));
+        if (posted > 32) reached += __popc(__ballot_sync(0xffffffffu, p1 >= v));
+        if (posted > 64) reached += __popc(__ballot_sync(0xffffffffu, p2 >= v));
+        if (reached >= topk) {             // the warp's largest such value
+            if (lane == 0) atomicMax(cut, v);
+            break;
+        }
+    }
+    __syncthreads();
+    return *cut;
+}
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
@@ -321,7 +340,9 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
     __shared__ float4 parts[kWarps];
     __shared__ float4 block_part;
     __shared__ uint32_t bound[kWarps];
-    __shared__ __align__(16) uint32_t posts[TOPK ? kPosts : 4];
+    __shared__ uint32_t posts[TOPK ? kPosts : 1], cut[2];
+    __shared__ unsigned long long cut_key;
+    __shared__ int kept;
     __shared__ __align__(16) uint64_t cand[TOPK ? kWarps * 32 : 1];     // kTeams * 32 at least
     __shared__ uint64_t best[TOPK ? kTeams : 1][32];
     __shared__ int count[kTeams];
@@ -373,6 +394,11 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
     if (TOPK) {
         if (lane == 0) bounds[warp] = 0;
         if (t == 0) count[team] = 0;
+        if (threadIdx.x == 0) {
+            cut[0] = cut[1] = 0;
+            cut_key = 0;
+            kept = 0;
+        }
         if (t < 32) best[team][t] = 0ull;
     }
 
@@ -430,39 +456,32 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
             const uint32_t bo = i0 < nvec && bm == bm ? order_of(bm) : 0u;
             if (first) {
                 // The lanes' maxima are distinct elements: the topk-th largest of some of
-                // them is a bound.  One warp takes it from all of its own; several post
-                // their `r` largest each, 2 topk of the block or more.
-                int above = 0;
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    const uint32_t o = __shfl_sync(0xffffffffu, bo, j);
-                    above += (o > bo || (o == bo && j < lane)) ? 1 : 0;
-                }
-                uint32_t cut = above == topk - 1 ? bo : 0u;
-                if (nw > 1) {
-                    cut = 0;
-                    const int r = (2 * topk + nw - 1) / nw;
-                    if (above < r) posts[warp * r + above] = bo;
-                    __syncthreads();
-                    const int posted = nw * r;     // at most 79
-                    uint32_t mine[3];
-                    int reached[3] = {0, 0, 0};
-#pragma unroll
-                    for (int i = 0; i < 3; ++i) mine[i] = lane + 32 * i < posted ? posts[lane + 32 * i] : 0u;
-                    for (int j = 0; j < posted; j += 4) {
-                        uint4 q = *reinterpret_cast<const uint4*>(&posts[j]);
-                        q.y = j + 1 < posted ? q.y : 0u;
-                        q.z = j + 2 < posted ? q.z : 0u;
-                        q.w = j + 3 < posted ? q.w : 0u;
-#pragma unroll
-                        for (int i = 0; i < 3; ++i)
-                            reached[i] += (q.x >= mine[i]) + (q.y >= mine[i]) + (q.z >= mine[i]) + (q.w >= mine[i]);
+                // them is a bound.  One warp takes it from its own; several post their `r`
+                // largest each, 2 topk of the block or more.
+                const int r = nw == 1 ? topk : (2 * topk + nw - 1) / nw;
+                uint32_t value = 0;                    // lane i: the i-th largest lane maximum
+                if (r <= 8) {
+                    uint32_t left = bo;
+                    for (int i = 0; i < r; ++i) {
+                        const uint32_t m = __reduce_max_sync(0xffffffffu, left);
+                        if (lane == __ffs(__ballot_sync(0xffffffffu, left == m)) - 1) left = 0;
+                        if (lane == i) value = m;
                     }
+                } else {
+                    int above = 0;
 #pragma unroll
-                    for (int i = 0; i < 3; ++i)
-                        if (reached[i] >= topk) cut = max(cut, mine[i]);
+                    for (int j = 0; j < 32; ++j) {
+                        const uint32_t o = __shfl_sync(0xffffffffu, bo, j);
+                        above += (o > bo || (o == bo && j < lane)) ? 1 : 0;
+                    }
+                    for (int i = nw == 1 ? r - 1 : 0; i < r; ++i) {
+                        const uint32_t who = __ballot_sync(0xffffffffu, above == i);
+                        const uint32_t m = __shfl_sync(0xffffffffu, bo, __ffs(who) - 1);
+                        if (lane == i) value = m;
+                    }
                 }
-                reach0 = __reduce_max_sync(0xffffffffu, cut);
+                reach0 = nw == 1 ? __shfl_sync(0xffffffffu, value, topk - 1)
+                                 : block_bound(posts, &cut[0], value, r, nw, topk, warp, lane);
             }
             uint32_t reach = max(reach0, __reduce_min_sync(0xffffffffu, bounds[lane & (nw - 1)]));
             // own entries of earlier rounds have lower indices: an equal logit loses to them
@@ -498,10 +517,15 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
 
     p.warp_join();
     if (nw > 1 && lane == 0) parts[warp] = make_float4(p.m, p.n, p.l, p.sa);
-    if (TOPK && rounds == 0) sync();   // (the counter's start; the first round had a barrier)
     if (TOPK) {
+        if (nw > 1) {                  // the same bound from the lists, so that few more than topk keys are ranked
+            const uint32_t mine = top.order();
+            reach0 = max(reach0, block_bound(posts, &cut[1], mine, (2 * topk + nw - 1) / nw, nw, topk, warp, lane));
+        } else {
+            __syncwarp();              // (the counter's start)
+        }
         // a list's entries that reach the bound, in front of it: topk at most, as no more can be asked for
-        const uint32_t mine = __ballot_sync(0xffffffffu, lane < topk && top.key != 0 && static_cast<uint32_t>(top.key >> 32) >= reach0);
+        const uint32_t mine = __ballot_sync(0xffffffffu, lane < topk && top.key != 0 && top.order() >= reach0);
         int at = 0;
         if (lane == 0 && mine) at = atomicAdd(&count[team], __popc(mine));
         at = __shfl_sync(0xffffffffu, at, 0);
@@ -529,13 +553,16 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
             }
             if (TOPK) {
                 // (a block of a split row has 8 warps or more: one warp per rank)
-                for (int k = warp; k < ranks; k += nw) {
-                    const uint64_t c = ld_cluster_u64(map_to_cta(smem_u32(&best[0][lane]), static_cast<uint32_t>(k)));
-                    if (lane < topk) cand[k * topk + lane] = c;
-                }
-                sync();
-                rank_keys(cand, ranks * topk, topk, best[0], t, row_threads);
-                sync();
+                uint64_t k = 0;
+                if (warp < ranks) k = ld_cluster_u64(map_to_cta(smem_u32(&best[0][lane]), static_cast<uint32_t>(warp)));
+                if (lane >= topk) k = 0;
+                // each rank's topk-th is a bound
+                if (lane == topk - 1 && k != 0) atomicMax(&cut_key, static_cast<unsigned long long>(k));
+                __syncthreads();
+                if (k != 0 && k >= cut_key) cand[atomicAdd(&kept, 1)] = k;
+                __syncthreads();
+                rank_keys(cand, kept, topk, best[0], t, row_threads);
+                __syncthreads();
             }
         }
         cluster_arrive();              // rank 0 has read the others' shared memory

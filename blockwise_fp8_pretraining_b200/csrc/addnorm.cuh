@@ -1,21 +1,29 @@
-// Residual addition, RMSNorm and the E4M3 quantization of its output in one
-// pass over the data, and the gradient through the norm.
+// Residual addition, RMSNorm and the E4M3 quantization of its output, and the
+// gradient through the norm.
 //
 //   s    = bf16(x + residual)                  (s = x without a residual)
 //   r    = fp32(1 / sqrt(mean_k s[k]^2 + eps))   per row, FP64 sum of squares
 //   y[k] = bf16(gamma[k] * bf16(fp32(s[k] * r)))
 //   codes and scales of y in 1x128 groups (and 128x1 groups along tokens)
 //
-// (rmsnorm.cuh has the same r and y for a given x; here the row's values stay
-// on the chip between the statistic and the quantization, so s is read zero
-// times instead of twice.)  bf16(x + residual) and bf16(gamma * t) are one
-// packed bfloat16 instruction each: a single rounding to nearest even of the
-// exact sum or product, subnormals kept.
+// (rmsnorm.cuh has the same r and y for a given x; here a row's values stay on
+// the chip between the statistic and the row-wise codes, so s is read zero
+// times instead of twice.  Groups along tokens take a second launch, which reads
+// s from the L2 cache.)  bf16(x + residual) and bf16(gamma * t) are one packed
+// bfloat16 instruction each: a single rounding to nearest even of the exact sum
+// or product, subnormals kept.
+//
+// All of it is bound by HBM: x, the residual, s and the codes, 6 to 8 bytes an
+// element.  On a B200, [8192, 2048]: row-wise 22.3 us (5.3 TB/s, 0.82 of a plain
+// copy's rate), both groupings 31.8 us; [1037, 6144] row-wise 11.5 us; one token
+// 2.1 us.
 //
 // Gradient, with n = s r and g = gamma dy for the gradient dy of y, the
 // roundings of the forward pass passed straight through:
 //   ds     = r (g - n mean_k(g n)) + dresidual
 //   dgamma = sum over rows of dy n
+// 8 bytes an element; [8192, 2048] 27.4 us (4.9 TB/s) with the launch that adds up
+// the blocks' shares of dgamma (about 3 us).
 #pragma once
 
 #include <cuda_bf16.h>

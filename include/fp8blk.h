@@ -214,7 +214,7 @@ fp8_status fp8_rmsnorm_quantize_1x128(const void *x_bf16, int64_t rows, int64_t 
 #define FP8_MAX_NORM_COLS 16384
 
 /*
- * Residual addition, RMSNorm and quantization in one pass over the data:
+ * Residual addition, RMSNorm and quantization, x and the residual read once:
  * s = bf16(x + residual) (one rounding to nearest even), rstd and y as in
  * fp8_rmsnorm_rstd and fp8_rmsnorm_quantize_1x128 of s, and the codes and
  * scales of y.  Given the rstd it writes, the codes and scales equal those of

@@ -41,8 +41,10 @@
 //
 // The tiles of a last, partly filled wave are cut where there are pairs for the
 // pieces: into two halves of 128 columns, whose epilogues are half as long (their
-// products are not: a stage of 128 columns takes the same 512 clocks as one of
-// 256, because each commit holds up the next products' issue), and along the
+// stages hardly are: with both operands in shared memory its bandwidth, 32 KB
+// written and 32 to 48 KB read a stage, bounds a stage of 256 columns at 576
+// clocks, where the tensor cores need 512, and one of 128 columns still at 505, by
+// two issuing threads; by one its commits hold it at 576), and along the
 // contraction, where the parts before the last leave their FP32 sums in the
 // workspace and the pair with the last one adds them in order.
 //

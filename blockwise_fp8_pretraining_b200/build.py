@@ -20,7 +20,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfp8blk.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("fp8blk.cu", "gemm.cuh", "quantize.cuh", "ptx.cuh", "swiglu.cuh", "rmsnorm.cuh",
-                                              "addnorm.cuh", "logprobs.cuh", "newton_schulz.cuh")]
+                                              "addnorm.cuh", "logprobs.cuh", "newton_schulz.cuh",
+                                              "newton_schulz_small.cuh")]
 HOST_SOURCE = os.path.join(CSRC, "host.cpp")
 # (its name says which torch and Python it was built for)
 HOST_LIB = os.path.join(HERE, f"_fp8blk_host.torch{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")

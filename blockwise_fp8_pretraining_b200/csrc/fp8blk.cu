@@ -15,11 +15,13 @@
 #include "gemm.cuh"
 #include "logprobs.cuh"
 #include "newton_schulz.cuh"
+#include "newton_schulz_small.cuh"
 #include "quantize.cuh"
 
 static_assert(fp8blk::kErrTimeout == static_cast<unsigned int>(FP8_ERR_TIMEOUT),
               "device time-out code must match the C ABI");
 static_assert(fp8blk::logp::kMaxTopK == FP8_MAX_TOPK, "alternatives limit must match the C ABI");
+static_assert(fp8blk::ns::small::kMaxSteps == FP8_NS_MAX_STEPS, "steps limit must match the C ABI");
 static_assert(fp8blk::addnorm::kMaxCols == FP8_MAX_NORM_COLS, "row length limit must match the C ABI");
 
 namespace {
@@ -359,11 +361,12 @@ bool dims_ok_gemm(int64_t M, int64_t N, int64_t K, bool m_positive) {
 
 // As launch_pdl, in clusters of `ranks` CTAs.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, unsigned ranks, cudaStream_t stream,
-                               Args... args) {
+cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, unsigned ranks,
+                               cudaStream_t stream, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -513,7 +516,7 @@ fp8_status launch_logp(const void* logits, int64_t rows, int64_t vocab, int64_t 
     float2* st2 = reinterpret_cast<float2*>(stats);
     const dim3 blocks(static_cast<unsigned>(grid)), block(static_cast<unsigned>(threads * teams));
     const cudaError_t e =
-        ranks > 1 ? launch_pdl_cluster(kernel, blocks, block, static_cast<unsigned>(ranks), s, x, rows, vocab, ld,
+        ranks > 1 ? launch_pdl_cluster(kernel, blocks, block, 0, static_cast<unsigned>(ranks), s, x, rows, vocab, ld,
                                        targets, topk, ranks, warps, logprob, entropy, st2, top_logprob, top_index)
                   : launch_pdl(kernel, blocks, block, 0, s, x, rows, vocab, ld, targets, topk, ranks, warps, logprob,
                                entropy, st2, top_logprob, top_index);
@@ -652,6 +655,107 @@ fp8_status launch_ns_cast(const T* g, int64_t batch, int64_t m, int64_t n, int64
                    static_cast<int>(parts), eps, scale, hi, lo, flags, num_flags);
     if (e != cudaSuccess) return cuda_fail("newton-schulz cast launch", e);
     return last_launch_status("newton-schulz cast launch");
+}
+
+std::atomic<int> g_ns_small_attr_done[kMaxDevices];
+std::atomic<int> g_ns_small_clusters[kMaxDevices][ns::small::kMaxRanks + 1];
+
+template <typename T>
+fp8_status ns_small_ready(int dev) {
+    constexpr int bit = sizeof(T) == 4 ? 1 : 2;
+    if ((g_ns_small_attr_done[dev].load(std::memory_order_acquire) & bit) == 0) {
+        const cudaError_t e = cudaFuncSetAttribute(ns::small::iterate_kernel<T>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, ns::small::kMaxSmem);
+        if (e != cudaSuccess) return cuda_fail("cudaFuncSetAttribute(newton-schulz, small)", e);
+        g_ns_small_attr_done[dev].fetch_or(bit, std::memory_order_release);
+    }
+    return FP8_OK;
+}
+
+// How many clusters of `ranks` CTAs run at once (a CTA fills its SM: its registers do).
+template <typename T>
+fp8_status ns_small_clusters(int dev, int sms, int ranks, int* clusters) {
+    *clusters = ranks == 1 ? sms : g_ns_small_clusters[dev][ranks].load(std::memory_order_acquire);
+    if (*clusters > 0) return FP8_OK;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(ranks));
+    cfg.blockDim = dim3(ns::small::kThreads);
+    cfg.dynamicSmemBytes = ns::small::kMaxSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaOccupancyMaxActiveClusters(clusters, ns::small::iterate_kernel<T>, &cfg);
+    if (e != cudaSuccess) return cuda_fail("cudaOccupancyMaxActiveClusters(newton-schulz, small)", e);
+    if (*clusters < 1) *clusters = 1;
+    g_ns_small_clusters[dev][ranks].store(*clusters, std::memory_order_release);
+    return FP8_OK;
+}
+
+// Whether one launch of clusters takes a batch (share > 0), and how it divides a
+// matrix.  128 columns of X per CTA finish one matrix sooner than 256 (s x l = 64 x
+// 512: 43 against 55 us; not up to s = 48: 42 and 42), but half as many matrices run
+// at once, so 256 where that saves a round of clusters (32 x 64 x 1024: 55 against
+// 129 us).  Rounds follow one another, while the launch per product spreads a batch
+// over tensor cores that a single matrix leaves idle: of matrices of three CTAs or
+// more it wins from about rounds x s = 192 on (36 x 128 x 1024: 152 against 188 us; 148
+// x 64 x 1024: 276 against 291; but 74 x 96 x 768: 161 against 139), of two with s > 64
+// from 256 on (300 x 128 x 512: 412 against 503; but 148: 216 against 203, and 600 x 64 x
+// 512: 584 against 535), of one never (1200 x 128 x 128: 573 against 453).  Its tiles are
+// 128 rows high, so up to s = 48 it does not win either (148 x 48 x 1024: 266 against
+// 217), or by no more than 7% (200 x 20 x 2048: 578 against 620).
+template <typename T>
+fp8_status ns_small_plan(int dev, int sms, int64_t batch, int s, int l, int* ranks, int* share) {
+    const fp8_status ready = ns_small_ready<T>(dev);
+    if (ready != FP8_OK) return ready;
+    int64_t best = 0;
+    for (int columns = s <= 48 ? 256 : 128; columns <= ns::small::kShare; columns *= 2) {
+        int r = (l + columns - 1) / columns;
+        if (r > ns::small::kMaxRanks) r = ns::small::kMaxRanks;
+        const int each = ns::small::up16((l + r - 1) / r);
+        r = (l + each - 1) / each;                           // none without columns
+        int clusters = 0;
+        const fp8_status st = ns_small_clusters<T>(dev, sms, r, &clusters);
+        if (st != FP8_OK) return st;
+        const int64_t rounds = (batch + clusters - 1) / clusters;
+        if (best != 0 && rounds >= best) continue;
+        best = rounds;
+        *ranks = r;
+        *share = each;
+    }
+    const bool many = *ranks > 2 ? s > 48 && best * s > 192 : *ranks == 2 && s > 64 && best * s > 256;
+    if (many) *share = 0;
+    return FP8_OK;
+}
+
+// Small matrices, one launch.
+template <typename T>
+fp8_status launch_ns_small(const void* g, int64_t batch, int64_t m, int64_t n, const float* coefficients, int steps,
+                           float eps, float scale, void* out, int ranks, int share, cudaStream_t s) {
+    ns::small::Params p{};
+    p.m = static_cast<int>(m);
+    p.n = static_cast<int>(n);
+    p.tall = m > n;
+    p.s = p.tall ? p.n : p.m;
+    p.l = p.tall ? p.m : p.n;
+    p.ranks = ranks;
+    p.share = share;
+    p.steps = steps;
+    p.eps = eps;
+    p.scale = scale;
+    for (int i = 0; i < 3 * steps; ++i) p.coeff[i] = coefficients[i];
+    auto kernel = ns::small::iterate_kernel<T>;
+    const dim3 grid(static_cast<unsigned>(batch * p.ranks)), block(ns::small::kThreads);
+    const size_t smem = static_cast<size_t>(ns::small::smem_bytes(p.s, p.share));
+    const T* x = static_cast<const T*>(g);
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(out);
+    const cudaError_t e = p.ranks > 1 ? launch_pdl_cluster(kernel, grid, block, smem, static_cast<unsigned>(p.ranks), s, x, y, p)
+                                      : launch_pdl(kernel, grid, block, smem, s, x, y, p);
+    if (e != cudaSuccess) return cuda_fail("newton-schulz launch (small)", e);
+    return last_launch_status("newton-schulz launch (small)");
 }
 
 // Scratch of fp8_block_gemm_wgrad_static_ws: the split schedule's workspace
@@ -939,6 +1043,18 @@ fp8_status fp8_newton_schulz(const void* g, int dtype, int64_t batch, int64_t m,
     // (entries of X up to 8 then stay inside FP16's range).
     float scale = 1.0f;
     while (scale < 8192.0f && 4.0 * scale * scale <= static_cast<double>(m) * static_cast<double>(n)) scale *= 2.0f;
+    if (ns::small::takes(m, n)) {
+        const int shorter = static_cast<int>(m < n ? m : n), longer = static_cast<int>(m < n ? n : m);
+        const bool f32 = dtype == FP8_F32;
+        int ranks = 0, share = 0;
+        st = f32 ? ns_small_plan<float>(dev, sms, batch, shorter, longer, &ranks, &share)
+                 : ns_small_plan<__nv_bfloat16>(dev, sms, batch, shorter, longer, &ranks, &share);
+        if (st != FP8_OK) return st;
+        if (share > 0)
+            return f32 ? launch_ns_small<float>(g, batch, m, n, coefficients, steps, eps, scale, out_bf16, ranks, share, s)
+                       : launch_ns_small<__nv_bfloat16>(g, batch, m, n, coefficients, steps, eps, scale, out_bf16, ranks,
+                                                        share, s);
+    }
     double* partial = reinterpret_cast<double*>(ws + w.partial);
     int* flags = reinterpret_cast<int*>(ws + w.flags);
     const int num_flags = w.slots * 2 * ns::EPI_WARPS;

@@ -54,8 +54,8 @@
 // 2048] 272 us.  A product's stages take 0.30 us each at full clock (the tensor
 // cores' 512 clocks are 0.27); around them stand about 1.5 us until the first
 // operands arrive, 2 to 4 us of epilogue and 1.5 us between kernels, which is
-// what bounds small matrices ([6, 520, 1100] 195 us, 13 us a product; anything
-// under 256 on both sides 85 to 105 us).
+// what bounds matrices of a few hundred rows ([6, 520, 1100] 195 us, 13 us a
+// product).  Smaller ones take one launch for all steps (newton_schulz_small.cuh).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -690,10 +690,27 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const T* __restrict_
     if (threadIdx.x == 0) partial[static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = sum;
 }
 
+// Multiplication by scale / norm, as two powers of two and a value in [1, 2), so
+// that neither a tiny nor a huge norm overflows or loses digits.  A zero norm
+// gives zeros, a non-finite one NaN.
+struct Factor {
+    float p1 = 1.0f, p2 = 1.0f, fr;
+    __device__ __forceinline__ Factor(double norm, float scale) {
+        const double f = norm > 0.0 ? static_cast<double>(scale) / norm : norm == norm ? 0.0 : norm;
+        if (f > 0.0 && f < 1e300) {
+            int e;
+            fr = static_cast<float>(frexp(f, &e));
+            p1 = scalbnf(1.0f, e / 2);
+            p2 = scalbnf(1.0f, e - e / 2);
+        } else {
+            fr = static_cast<float>(f);
+        }
+    }
+    __device__ __forceinline__ float operator()(float v) const { return v * p1 * p2 * fr; }
+};
+
 // hi[z][row][0 .. ld) = FP16(v) and lo = FP16(v - hi) of v = g * scale / (norm
 // + eps), columns behind n zero.
-// The factor is applied as two powers of two and a value in [1, 2), so that
-// neither a tiny nor a huge norm overflows or loses digits.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kNormThreads)
     cast_kernel(const T* __restrict__ g, int rows, int n, int ld, const double* __restrict__ partial, int parts,
@@ -707,18 +724,7 @@ __global__ void __launch_bounds__(kNormThreads)
         for (int i = threadIdx.x; i < num_flags; i += kNormThreads) flags[i] = 0;
     double mine = 0.0;
     for (int i = threadIdx.x; i < parts; i += kNormThreads) mine += partial[z * parts + i];
-    const double norm = sqrt(block_sum(mine, red)) +
-                        static_cast<double>(eps);
-    double f = norm > 0.0 ? static_cast<double>(scale) / norm : norm == norm ? 0.0 : norm;
-    float p1 = 1.0f, p2 = 1.0f, fr;
-    if (f > 0.0 && f < 1e300) {
-        int e;
-        fr = static_cast<float>(frexp(f, &e));
-        p1 = scalbnf(1.0f, e / 2);
-        p2 = scalbnf(1.0f, e - e / 2);
-    } else {
-        fr = static_cast<float>(f);
-    }
+    const Factor factor(sqrt(block_sum(mine, red)) + static_cast<double>(eps), scale);
     const int64_t per_row = ld / 8, total = static_cast<int64_t>(rows) * per_row;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kNormThreads + threadIdx.x; i < total;
          i += static_cast<int64_t>(gridDim.x) * kNormThreads) {
@@ -742,8 +748,8 @@ __global__ void __launch_bounds__(kNormThreads)
         uint32_t w[4], l[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float v0 = c + 2 * j < n ? v[2 * j] * p1 * p2 * fr : 0.0f;
-            const float v1 = c + 2 * j + 1 < n ? v[2 * j + 1] * p1 * p2 * fr : 0.0f;
+            const float v0 = c + 2 * j < n ? factor(v[2 * j]) : 0.0f;
+            const float v1 = c + 2 * j + 1 < n ? factor(v[2 * j + 1]) : 0.0f;
             const __half2 h = __floats2half2_rn(v0, v1);
             w[j] = *reinterpret_cast<const uint32_t*>(&h);
             const float2 back = __half22float2(h);

@@ -356,8 +356,10 @@ fp8_status fp8_token_logprobs_backward(const void *logits, int dtype, int64_t ro
  * two steps carry X in two FP16 parts) with FP32 accumulation; with the usual
  * coefficients, whose X stays below about 1.3 in spectral norm, no value
  * leaves FP16's range.  Coefficients that let entries of X grow past 4 give
- * infinities.  A zero matrix gives zeros; a non-finite
- * element makes its whole matrix NaN.  Results repeat run to run.  Passage:
+ * infinities.  A zero matrix gives zeros, and one whose norm
+ * is below about 2^-14 eps loses digits of its (equally small) result, down to
+ * zeros, as X leaves FP16's range; a non-finite element makes its whole matrix
+ * NaN.  Results repeat run to run.  Passage:
  * Puro-2B-Base model card (friendli.ai), training-setup paragraph (MuonH on
  * the matrices, FP32 optimizer state); the pages give neither the iteration
  * nor its coefficients, so this is the published Muon iteration with the

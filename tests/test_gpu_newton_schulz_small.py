@@ -128,3 +128,15 @@ def test_many(shape):
     assert torch.equal(fp8.fp8_newton_schulz(g), out)
     for i in (0, 1, shape[0] // 2, shape[0] - 1):
         check(g[i], out[i], noise=min(shape[1:]) >= 64)
+
+
+@pytest.mark.parametrize("shape", [(40, 90), (300, 280)])
+def test_norm_far_below_eps(shape):
+    """X is then |G| / eps times a unit matrix, and each step multiplies it by at most
+    a = 3.4445 (its cube no longer counts): digits may be lost, nothing may be made up.
+    FP16 in its subnormals, of X times more than sqrt(mn) / 2, is off by 2^-25 an element,
+    2^-24 of the norm, at the start and after each step: 2^-24 (a^5 + a^4 + ...) < 2^-23 a^5."""
+    g = gaussian(shape, 5)
+    for norm in (1e-13, 1e-20):
+        out = fp8.fp8_newton_schulz(g * (norm / float(g.norm()))).double()
+        assert float(out.norm()) <= 1.01 * (norm / 1e-7) * 3.4445 ** 5 + 3.4445 ** 5 * 2.0 ** -23

@@ -712,7 +712,7 @@ fp8_status ns_small_plan(int dev, int sms, int64_t batch, int s, int l, int* ran
     const fp8_status ready = ns_small_ready<T>(dev);
     if (ready != FP8_OK) return ready;
     int64_t best = 0;
-    for (int columns = s <= 48 ? 256 : 128; columns <= ns::small::kShare; columns *= 2) {
+    for (int columns = s <= 48 ? 256 : 128; columns <= 256; columns *= 2) {
         int r = (l + columns - 1) / columns;
         if (r > ns::small::kMaxRanks) r = ns::small::kMaxRanks;
         const int each = ns::small::up16((l + r - 1) / r);

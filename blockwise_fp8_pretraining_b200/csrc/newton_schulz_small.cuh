@@ -1,6 +1,7 @@
 // Newton-Schulz orthogonalisation of small matrices in one launch: a shorter
-// side s of up to 128 and a longer side l of up to 2048 (the iteration and its
-// roundings are newton_schulz.cuh's).
+// side s of up to 128 and a longer side l of up to 8192 as far as a CTA's shared
+// memory holds an eighth of it, which is 2432 at s = 128, 6528 at 64 and all at 48
+// (the iteration and its roundings are newton_schulz.cuh's).
 //
 // There every product is a launch, and on matrices this small a launch is all
 // there is: some 5.5 us of set-up, first load, epilogue and exit for well under a
@@ -20,6 +21,9 @@
 //   17 x 17    16 against 63      64 x 500   43 against 87      128 x 1000   73 against 105
 //   64 x 64    24 against 68     128 x 128   45 against 82      128 x 2048  100 against 120
 //   32 x 1000  42 against 90     128 x 500   68 against 98     2000 x 100    90 against 124
+//   32 x 4096  61 against 105     64 x 4096  86 against 107     128 x 2112  114 against 120
+//   32 x 8192 103 against 120     64 x 6144 116 against 117      96 x 3500  107 against 128
+// (beyond 8192 the few warps that S has tiles for at such s take too long).
 // (The entry point says how many matrices at a time are worth it.)
 #pragma once
 
@@ -29,8 +33,7 @@ namespace fp8blk {
 namespace ns {
 namespace small {
 
-constexpr int kMaxShort = 128, kMaxLong = 2048, kMaxRanks = 8;
-constexpr int kShare = kMaxLong / kMaxRanks;      // columns of X per CTA, at most
+constexpr int kMaxShort = 128, kMaxLong = 8192, kMaxRanks = 8;
 constexpr int kTiles = 4;                         // of 16 x 16, a warp's piece of a product at a time
 constexpr int kThreads = 512;
 constexpr int kMaxSteps = 32;
@@ -52,11 +55,12 @@ __host__ __device__ constexpr int up16(int v) { return (v + 15) / 16 * 16; }
 __host__ __device__ constexpr int x_bytes(int sp, int share) { return sp * (share + 8) * 2; }
 __host__ __device__ constexpr int s_bytes(int sp) { return sp * (sp + 8) * 2; }
 constexpr int smem_bytes(int s, int share) { return 2 * x_bytes(up16(s), share) + 2 * s_bytes(up16(s)); }
-constexpr int kMaxSmem = smem_bytes(kMaxShort, kShare);
+constexpr int kMaxSmem = 227 * 1024 - 1024;       // what a CTA may have, without the static part
 
 inline bool takes(int64_t m, int64_t n) {
     const int64_t s = m < n ? m : n, l = m < n ? n : m;
-    return s <= kMaxShort && l <= kMaxLong;
+    return s <= kMaxShort && l <= kMaxLong &&
+           smem_bytes(static_cast<int>(s), up16(static_cast<int>(l + kMaxRanks - 1) / kMaxRanks)) <= kMaxSmem;
 }
 
 template <bool TRANS>
@@ -190,8 +194,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int fr = lane >> 2, fc = 2 * (lane & 3);                        // its fragment's row and column
     const int s_first = group * row_tiles / groups, s_c0 = 16 * s_first;
     const int s_tiles = r0 < sp ? (group + 1) * row_tiles / groups - s_first : 0;
-    // X in one pass, or in two halves of its columns where a warp has more than kTiles
-    const int x_half = lp / 16 > groups * kTiles ? (lp / 16 + 1) / 2 : lp / 16;
+    // X in as many passes over its columns as leave a warp kTiles at most
+    const int passes = (lp / 16 + groups * kTiles - 1) / (groups * kTiles), x_pass = (lp / 16 + passes - 1) / passes;
     const float alpha = 1.0f / (p.scale * p.scale), back = 1.0f / p.scale;
 
     for (int k = 0; k < p.steps; ++k) {
@@ -270,8 +274,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncthreads();
         // ------------------------------------------------------------------ X
-        for (int from = 0; from < lp / 16; from += x_half) {
-            const int tiles = min(x_half, lp / 16 - from), first = group * tiles / groups;
+        for (int from = 0; from < lp / 16; from += x_pass) {
+            const int tiles = min(x_pass, lp / 16 - from), first = group * tiles / groups;
             const int x_tiles = r0 < sp ? (group + 1) * tiles / groups - first : 0, x_c0 = 16 * (from + first);
             float acc[2 * kTiles][4];
             if (x_tiles > 0) product<false>(acc, Q, lds, r0, xh, ldx, x_c0, x_tiles, sp, lane);

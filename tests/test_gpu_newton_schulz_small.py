@@ -1,6 +1,6 @@
 """Newton-Schulz on matrices small enough for one launch (a shorter side of up to
-128, a longer one of up to 2048), at every number of CTAs a matrix takes, at the
-edges of the range and just behind them.  Bounds as in the iteration's own tests:
+128, a longer one of 2432 there and of up to 8192 at 48), at every number of CTAs a
+matrix takes, at the edges of the range and just behind them.  Bounds as in the iteration's own tests:
 the roundings are the same."""
 import math
 
@@ -140,3 +140,22 @@ def test_norm_far_below_eps(shape):
     for norm in (1e-13, 1e-20):
         out = fp8.fp8_newton_schulz(g * (norm / float(g.norm()))).double()
         assert float(out.norm()) <= 1.01 * (norm / 1e-7) * 3.4445 ** 5 + 3.4445 ** 5 * 2.0 ** -23
+
+
+# The longest that fit a cluster's shared memory, and the first that do not.
+@pytest.mark.parametrize("shape", [(128, 2432), (128, 2433), (112, 3000), (96, 3840), (96, 3841), (80, 4992), (80, 4999),
+                                   (65, 4900), (64, 6528), (64, 6529), (48, 8191), (48, 8192), (48, 8193), (33, 5000)])
+def test_longest(shape):
+    for dtype in (torch.float32, torch.bfloat16):
+        g = gaussian(shape, sum(shape), dtype)
+        check(g, fp8.fp8_newton_schulz(g), noise=shape[0] >= 64)
+        tall = g.T.contiguous()
+        check(tall, fp8.fp8_newton_schulz(tall), noise=shape[0] >= 64)
+
+
+@pytest.mark.parametrize("shape", [(1, 8192), (3, 8001), (17, 8192), (32, 7777)])
+def test_longest_thin(shape):
+    g = gaussian((2, *shape), sum(shape))
+    out = fp8.fp8_newton_schulz(g)
+    check(g, out, noise=False)
+    assert torch.equal(out[0], fp8.fp8_newton_schulz(g[0].contiguous()))

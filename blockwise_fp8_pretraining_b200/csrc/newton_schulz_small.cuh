@@ -18,13 +18,13 @@
 // product the tensor memory's round trip would cost more than its rate gains.
 // Bound by latency: barriers, fragment loads and, for s near 128, mma.sync's rate.
 // One matrix, five steps, against the launch per product (us, graph replay):
-//   17 x 17    16 against 63      64 x 500   43 against 87      128 x 1000   73 against 105
-//   64 x 64    24 against 68     128 x 128   45 against 82      128 x 2048  100 against 120
-//   32 x 1000  42 against 90     128 x 500   68 against 98     2000 x 100    90 against 124
-//   32 x 4096  61 against 105     64 x 4096  86 against 107     128 x 2112  114 against 120
-//   32 x 8192 103 against 120     64 x 6144 116 against 117      96 x 3500  107 against 128
-// (beyond 8192 the few warps that S has tiles for at such s take too long).
-// (The entry point says how many matrices at a time are worth it.)
+//   17 x 17    13 against 63      64 x 500   33 against 87      128 x 1000   70 against 105
+//   64 x 64    17 against 68     128 x 128   43 against 82      128 x 2048   95 against 120
+//   32 x 1000  31 against 90     128 x 500   65 against 98     2000 x 100    84 against 124
+//   32 x 4096  42 against 105     64 x 4096  64 against 107     128 x 2112  102 against 120
+//   32 x 8192  66 against 120     64 x 6144  85 against 117      96 x 3500   93 against 128
+// (The entry point says how many matrices at a time are worth it.)  Of a step's 21,000
+// clocks at 128 x 1000, S takes 3,000, its exchange 10,000, Q 4,300 and X 5,300.
 #pragma once
 
 #include "newton_schulz.cuh"
@@ -79,10 +79,29 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// acc = 16 rows of A times NT tiles of 16 columns of B, over `steps` times 16 of k;
+// pa, pb: this lane's row of the first fragments, `tile` and `step` bytes on for the
+// next tile and the next 16 of k.
+template <int NT, bool B_K>
+__device__ __forceinline__ void product_of(float (&acc)[2 * kTiles][4], uint32_t pa, uint32_t pb, uint32_t tile, uint32_t step,
+                                           int steps) {
+#pragma unroll 2
+    for (int k = 0; k < steps; ++k) {
+        uint32_t fa[4], fb[NT][4];
+        ldmatrix4<false>(fa, pa + 32 * k);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) ldmatrix4<!B_K>(fb[t], pb + k * step + t * tile);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            mma16816(acc[2 * t], fa, fb[t][0], fb[t][1]);
+            mma16816(acc[2 * t + 1], fa, fb[t][2], fb[t][3]);
+        }
+    }
+}
+
 // acc = rows r0 .. + 15 of A times `tiles` (1 to kTiles) tiles of 16 columns of B
 // from c0 on, over k < K.  A: [row][k], rows of lda.  B: [column][k] (B_K) or
-// [k][column], rows of ldb.  All tiles' fragments are loaded together, the last one
-// again in the place of those that are not there (their sums are not used).
+// [k][column], rows of ldb.
 template <bool B_K>
 __device__ __forceinline__ void product(float (&acc)[2 * kTiles][4], const __half* a, int lda, int r0, const __half* b, int ldb,
                                         int c0, int tiles, int K, int lane) {
@@ -94,18 +113,12 @@ __device__ __forceinline__ void product(float (&acc)[2 * kTiles][4], const __hal
     const uint32_t pb = smem_u32(B_K ? b + (c0 + (lane & 7) + ((lane >> 4) << 3)) * ldb + ((lane >> 3) & 1) * 8
                                      : b + ((lane & 7) + ((lane >> 3) & 1) * 8) * ldb + c0 + (lane >> 4) * 8);
     const uint32_t tile = (B_K ? 16 * ldb : 16) * 2, step = (B_K ? 16 : 16 * ldb) * 2;      // bytes
-#pragma unroll 2
-    for (int k = 0; k < K / 16; ++k) {
-        uint32_t fa[4];
-        ldmatrix4<false>(fa, pa + 32 * k);
-        uint32_t fb[kTiles][4];
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) ldmatrix4<!B_K>(fb[t], pb + k * step + min(t, tiles - 1) * tile);
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-            mma16816(acc[2 * t], fa, fb[t][0], fb[t][1]);
-            mma16816(acc[2 * t + 1], fa, fb[t][2], fb[t][3]);
-        }
+    static_assert(kTiles == 4, "one case each");
+    switch (tiles) {                       // the same for the warp
+        case 1: product_of<1, B_K>(acc, pa, pb, tile, step, K / 16); break;
+        case 2: product_of<2, B_K>(acc, pa, pb, tile, step, K / 16); break;
+        case 3: product_of<3, B_K>(acc, pa, pb, tile, step, K / 16); break;
+        default: product_of<4, B_K>(acc, pa, pb, tile, step, K / 16); break;
     }
 }
 
@@ -147,27 +160,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t dj = p.tall ? p.n : 1;
     const T* src = g + at + c0 * dj;
     const int inner = p.tall ? p.s : cl, outer = p.tall ? cl : p.s;        // along and across memory's rows
-    // f(row, column in memory, value), four rows' loads at a time
-    auto each = [&](auto f) {
-        for (int o = warp; o < outer; o += 4 * (kThreads / 32))
-            for (int i = lane; i < inner; i += 32) {
-                float v[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int r = o + q * (kThreads / 32);
-                    v[q] = r < outer ? to_float(src[static_cast<int64_t>(r) * p.n + i]) : 0.0f;
-                }
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (o + q * (kThreads / 32) < outer) f(o + q * (kThreads / 32), i, v[q]);
-            }
-    };
+    for (int e = t; e < 2 * sp * ldx / 8; e += kThreads) reinterpret_cast<uint4*>(xh)[e] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+    // One pass over memory, eight rows' loads at a time: the norm, and the elements'
+    // upper and lower halves into X_hi's and X_lo's places.
+    constexpr int kAtOnce = 8;
     double sum = 0.0;
-    each([&](int, int, float v) { sum = fma(static_cast<double>(v), static_cast<double>(v), sum); });
+    for (int o = warp; o < outer; o += kAtOnce * (kThreads / 32))
+        for (int i = lane; i < inner; i += 32) {
+            float v[kAtOnce];
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) {
+                const int r = o + q * (kThreads / 32);
+                v[q] = r < outer ? to_float(src[static_cast<int64_t>(r) * p.n + i]) : 0.0f;
+            }
+#pragma unroll
+            for (int q = 0; q < kAtOnce; ++q) {
+                const int r = o + q * (kThreads / 32);
+                sum = fma(static_cast<double>(v[q]), static_cast<double>(v[q]), sum);
+                if (r < outer) {
+                    const uint32_t u = __float_as_uint(v[q]);
+                    const int at_x = p.tall ? i * ldx + r : r * ldx + i;
+                    reinterpret_cast<uint16_t*>(xh)[at_x] = static_cast<uint16_t>(u >> 16);
+                    reinterpret_cast<uint16_t*>(xl)[at_x] = static_cast<uint16_t>(u);
+                }
+            }
+        }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) red[warp] = sum;
-    for (int e = t; e < 2 * sp * ldx / 8; e += kThreads) reinterpret_cast<uint4*>(xh)[e] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     sum = 0.0;
     for (int w = 0; w < kThreads / 32; ++w) sum += red[w];
@@ -178,13 +199,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int r = 0; r < p.ranks; ++r) sum += ld_cluster_f64(map_to_cta(smem_u32(&share_sum), static_cast<uint32_t>(r)));
     }
     const Factor f(sqrt(sum) + static_cast<double>(p.eps), p.scale);
-    each([&](int r, int i, float g0) {
-        const float v = f(g0);
-        const __half h = __float2half_rn(v);
-        const int at_x = p.tall ? i * ldx + r : r * ldx + i;
-        xh[at_x] = h;
-        xl[at_x] = __float2half_rn(v - __half2float(h));
-    });
+    for (int e = t; e < sp * ldx / 2; e += kThreads) {       // two elements where they are; what is padding stays 0
+        uint32_t& h = reinterpret_cast<uint32_t*>(xh)[e];
+        uint32_t& l = reinterpret_cast<uint32_t*>(xl)[e];
+        const float v0 = f(__uint_as_float((h << 16) | (l & 0xFFFFu))), v1 = f(__uint_as_float((h & 0xFFFF0000u) | (l >> 16)));
+        const __half2 hi = __floats2half2_rn(v0, v1);
+        const float2 back2 = __half22float2(hi);
+        const __half2 lo = __floats2half2_rn(v0 - back2.x, v1 - back2.y);
+        h = *reinterpret_cast<const uint32_t*>(&hi);
+        l = *reinterpret_cast<const uint32_t*>(&lo);
+    }
     __syncthreads();
 
     // a warp's piece of a product: 16 rows, and its group's share of the columns

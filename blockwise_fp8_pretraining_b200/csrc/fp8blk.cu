@@ -697,22 +697,23 @@ fp8_status ns_small_clusters(int dev, int sms, int ranks, int* clusters) {
 
 // Whether one launch of clusters takes a batch (share > 0), and how it divides a
 // matrix.  128 columns of X per CTA finish one matrix sooner than 256 (s x l = 64 x
-// 512: 43 against 55 us; not up to s = 48: 42 and 42), but half as many matrices run
-// at once, so 256 where that saves a round of clusters (32 x 64 x 1024: 55 against
-// 129 us).  Rounds follow one another, while the launch per product spreads a batch
-// over tensor cores that a single matrix leaves idle: of matrices of three CTAs or
-// more it wins from about rounds x s = 192 on (36 x 128 x 1024: 152 against 188 us; 148
-// x 64 x 1024: 276 against 291; but 74 x 96 x 768: 161 against 139), of two with s > 64
-// from 256 on (300 x 128 x 512: 412 against 503; but 148: 216 against 203, and 600 x 64 x
-// 512: 584 against 535), of one never (1200 x 128 x 128: 573 against 453).  Its tiles are
-// 128 rows high, so up to s = 48 it does not win either (148 x 48 x 1024: 266 against
-// 217), or by no more than 7% (200 x 20 x 2048: 578 against 620).
+// 1024: 34 against 42 us, 96 x 512: 45 against 62), but half as many matrices run at
+// once, so 256 where that saves a round of clusters (32 x 64 x 1024: 43 against 102
+// us).  Rounds follow one another, while the launch per product spreads a batch over
+// tensor cores that a single matrix leaves idle.  Its tiles are 128 rows high: up to
+// s = 80 it does not win (300 x 64 x 1024: 556 against 446; 148 x 80 x 640: 220 against
+// 205), nor where a matrix has one CTA (1200 x 128 x 128: 573 against 453).  Else it
+// does where the last of several rounds would be short (36 x 128 x 1024, 34 at once:
+// 152 against 178; 100 x 100 x 640, 49 at once: 200 against 222; but 60 x 96 x 2500,
+// 15 at once: 394 against 324), and for many matrices that nearly fill its tiles (100 x
+// 128 x 1024: 281 against 366; 75 x 104 x 2048: 359 against 431; but 40 x 120 x 1500: 224
+// against 188, 60 x 128 x 1024: 190 against 183).
 template <typename T>
 fp8_status ns_small_plan(int dev, int sms, int64_t batch, int s, int l, int* ranks, int* share) {
     const fp8_status ready = ns_small_ready<T>(dev);
     if (ready != FP8_OK) return ready;
-    int64_t best = 0;
-    for (int columns = s <= 48 ? 256 : 128; columns <= 256; columns *= 2) {
+    int64_t best = 0, room = 0;
+    for (int columns = 128; columns <= 256; columns *= 2) {
         int r = (l + columns - 1) / columns;
         if (r > ns::small::kMaxRanks) r = ns::small::kMaxRanks;
         const int each = ns::small::up16((l + r - 1) / r);
@@ -723,11 +724,13 @@ fp8_status ns_small_plan(int dev, int sms, int64_t batch, int s, int l, int* ran
         const int64_t rounds = (batch + clusters - 1) / clusters;
         if (best != 0 && rounds >= best) continue;
         best = rounds;
+        room = rounds * clusters;
         *ranks = r;
         *share = each;
     }
-    const bool many = *ranks > 2 ? s > 48 && best * s > 192 : *ranks == 2 && s > 64 && best * s > 256;
-    if (many) *share = 0;
+    const bool short_last = s > 80 && *ranks > 1 && best > 1 && 4 * batch < 3 * room;
+    const bool many = s > 96 && *ranks > 2 && best > 1 && batch > 48;
+    if (short_last || many) *share = 0;
     return FP8_OK;
 }
 

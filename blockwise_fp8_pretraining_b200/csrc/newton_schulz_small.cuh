@@ -20,7 +20,7 @@
 // One matrix, five steps, against the launch per product (us, graph replay):
 //   17 x 17    13 against 63      64 x 500   33 against 87      128 x 1000   70 against 105
 //   64 x 64    17 against 68     128 x 128   43 against 82      128 x 2048   95 against 120
-//   32 x 1000  31 against 90     128 x 500   65 against 98     2000 x 100    84 against 124
+//   32 x 1000  26 against 90     128 x 500   65 against 98     2000 x 100    84 against 124
 //   32 x 4096  42 against 105     64 x 4096  64 against 107     128 x 2112  102 against 120
 //   32 x 8192  66 against 120     64 x 6144  85 against 117      96 x 3500   93 against 128
 // (The entry point says how many matrices at a time are worth it.)  Of a step's 21,000

@@ -752,7 +752,8 @@ fp8_status launch_ns_small(const void* g, int64_t batch, int64_t m, int64_t n, c
     for (int i = 0; i < 3 * steps; ++i) p.coeff[i] = coefficients[i];
     auto kernel = ns::small::iterate_kernel<T>;
     const dim3 grid(static_cast<unsigned>(batch * p.ranks)), block(ns::small::kThreads);
-    const size_t smem = static_cast<size_t>(ns::small::smem_bytes(p.s, p.share));
+    p.apart = ranks > 1 && ns::small::smem_bytes_apart(p.s, share) <= ns::small::kMaxSmem;
+    const size_t smem = static_cast<size_t>(p.apart ? ns::small::smem_bytes_apart(p.s, share) : ns::small::smem_bytes(p.s, share));
     const T* x = static_cast<const T*>(g);
     __nv_bfloat16* y = static_cast<__nv_bfloat16*>(out);
     const cudaError_t e = p.ranks > 1 ? launch_pdl_cluster(kernel, grid, block, smem, static_cast<unsigned>(p.ranks), s, x, y, p)

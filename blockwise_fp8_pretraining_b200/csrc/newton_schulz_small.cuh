@@ -18,13 +18,13 @@
 // product the tensor memory's round trip would cost more than its rate gains.
 // Bound by latency: barriers, fragment loads and, for s near 128, mma.sync's rate.
 // One matrix, five steps, against the launch per product (us, graph replay):
-//   17 x 17    13 against 63      64 x 500   33 against 87      128 x 1000   70 against 105
+//   17 x 17    13 against 63      64 x 500   31 against 87      128 x 1000   68 against 105
 //   64 x 64    17 against 68     128 x 128   43 against 82      128 x 2048   95 against 120
-//   32 x 1000  26 against 90     128 x 500   65 against 98     2000 x 100    84 against 124
-//   32 x 4096  42 against 105     64 x 4096  64 against 107     128 x 2112  102 against 120
-//   32 x 8192  66 against 120     64 x 6144  85 against 117      96 x 3500   93 against 128
+//   32 x 1000  25 against 90     128 x 500   63 against 98     2000 x 100    82 against 124
+//   32 x 4096  41 against 105     64 x 4096  61 against 107     128 x 2112  102 against 120
+//   32 x 8192  66 against 120     64 x 6144  82 against 117      96 x 3500   94 against 128
 // (The entry point says how many matrices at a time are worth it.)  Of a step's 21,000
-// clocks at 128 x 1000, S takes 3,000, its exchange 10,000, Q 4,300 and X 5,300.
+// clocks at 128 x 1000, S takes 3,000, its exchange 9,000, Q 4,300 and X 5,300.
 #pragma once
 
 #include "newton_schulz.cuh"
@@ -43,6 +43,7 @@ struct Params {
     int s, l;                   // shorter and longer side
     int tall;                   // more rows than columns
     int ranks, share;           // CTAs per matrix; columns of X per CTA (a multiple of 16)
+    int apart;                  // the FP32 share of S lies over Q alone
     int steps;
     float eps, scale;           // X is kept times scale
     float coeff[3 * kMaxSteps];
@@ -55,6 +56,12 @@ __host__ __device__ constexpr int up16(int v) { return (v + 15) / 16 * 16; }
 __host__ __device__ constexpr int x_bytes(int sp, int share) { return sp * (share + 8) * 2; }
 __host__ __device__ constexpr int s_bytes(int sp) { return sp * (sp + 8) * 2; }
 constexpr int smem_bytes(int s, int share) { return 2 * x_bytes(up16(s), share) + 2 * s_bytes(up16(s)); }
+// The same with the FP32 share over Q and what follows: S may then be handed round
+// while others still read their shares, which saves one barrier of the cluster (64 x 500: 33 to
+// 31 us, 128 x 1000: 70 to 68).
+constexpr int smem_bytes_apart(int s, int share) {
+    return 2 * x_bytes(up16(s), share) + s_bytes(up16(s)) + 4 * up16(s) * (up16(s) + 4);
+}
 constexpr int kMaxSmem = 227 * 1024 - 1024;       // what a CTA may have, without the static part
 
 inline bool takes(int64_t m, int64_t n) {
@@ -151,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __half* xl = xh + sp * ldx;
     __half* S = xl + sp * ldx;
     __half* Q = S + sp * lds;
-    float* part = reinterpret_cast<float*>(S);
+    float* part = reinterpret_cast<float*>(p.apart ? Q : S);
     static_assert(4 * (kMaxShort + 4) <= 2 * 2 * (kMaxShort + 8), "the FP32 share lies over S and Q");
 
     griddep_launch_dependents();
@@ -265,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     v[q] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
                 }
             }
-            cluster_sync();                // every share has been read: S may take its place
+            if (!p.apart) cluster_sync();  // every share has been read: S may take its place
 #pragma unroll
             for (int q = 0; q < kPasses; ++q) {
                 const int row = first + warp + q * (kThreads / 32);

@@ -479,6 +479,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
             if (last_part && others > 0) {
                 if (lane < others) got = flag_wait(flag(lane), p.product, abort_flag, p.wait_ns);
                 if (!__all_sync(0xffffffffu, got)) break;
+                __syncwarp();                      // what its lanes acquired holds for the warp (a vote orders no memory)
             }
             auto release = [&] {                   // the accumulator may be refilled
                 tc_fence_before();

@@ -4,7 +4,8 @@ compiled as well (csrc/host.cpp), for plain calls on the current stream.
 
 Every function here has the name of the C entry point it calls.  Tensors are
 torch CUDA tensors; outputs the caller does not pass are allocated with torch
-(device memory only: the library itself never allocates).  A non-zero status
+(device memory only: the library itself never allocates), from the pool of the
+stream the call runs on.  A non-zero status
 raises Fp8Error.  The library must have been built (``python -m
 blockwise_fp8_pretraining_b200.build``); there is no fallback.
 """
@@ -166,15 +167,30 @@ def _launch_checks(named, stream) -> None:
     _check_devices(named, torch.cuda.current_device(), stream)
 
 
-def _record(stream, allocated) -> None:
-    """Outputs allocated here belong to the current stream's pool; when the
-    kernel runs on another torch stream, tie their lifetime to that stream
-    too so their memory is not reused while the kernel still writes it.
-    (With a raw stream handle that is the caller's job.)"""
-    if isinstance(stream, torch.cuda.Stream):
-        for t in allocated:
-            if t is not None:
-                t.record_stream(stream)
+def _elsewhere(function, stream, *args, **kwargs):
+    """function(*args, **kwargs) with `stream` (a torch stream, or a handle on the
+    current device) as the current one.
+
+    What the call allocates then comes from that stream's pool, where whatever
+    used the memory before is ordered ahead of the kernel; memory freed on the
+    caller's stream may have work of that stream on it that is still to run.  New
+    outputs are also tied to the caller's stream, which will read them: when they
+    are freed, they are not reused before what is queued there has run."""
+    dev = torch.cuda.current_device()
+    launch = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device=dev)
+    _check_devices((), dev, launch)
+    caller = torch.cuda.current_stream()
+    if caller.cuda_stream == launch.cuda_stream:
+        return function(*args, **kwargs)
+    torch.cuda.set_stream(launch)
+    try:
+        out = function(*args, **kwargs)
+    finally:
+        torch.cuda.set_stream(caller)
+    for t in out if isinstance(out, tuple) else (out,):
+        if isinstance(t, torch.Tensor) and not any(t is given for given in args):
+            t.record_stream(caller)
+    return out
 
 
 def _ptr(t: torch.Tensor | None) -> int:
@@ -207,14 +223,14 @@ def fp8_quantize_act_1x128(x, mode=BOTH, q_row=None, s_row=None, q_colT=None, s_
                            stream=None):
     """Quantize a bf16 activation [rows, cols].  Returns (q_row, s_row,
     q_colT, s_col); entries of a grouping the mode leaves out are None."""
+    if stream is not None:
+        return _elsewhere(fp8_quantize_act_1x128, stream, x, mode, q_row, s_row, q_colT, s_col)
     lib = load()
     if x.dtype != torch.bfloat16 or x.dim() != 2:
         raise TypeError("x must be a 2-D bfloat16 tensor")
     rows, cols = x.shape
     _want(x, torch.bfloat16, (rows, cols), "x")
     dev = x.device
-    given_q_row, given_s_row = q_row is not None, s_row is not None
-    given_q_colT, given_s_col = q_colT is not None, s_col is not None
     if mode & ROWWISE:
         q_row = _out(q_row, torch.uint8, (rows, cols), dev, "q_row")
         s_row = _out(s_row, torch.float32, (cols // 128, rows), dev, "s_row")
@@ -227,8 +243,6 @@ def fp8_quantize_act_1x128(x, mode=BOTH, q_row=None, s_row=None, q_colT=None, s_
         q_colT = s_col = None
     _launch_checks([("x", x), ("q_row", q_row), ("s_row", s_row), ("q_colT", q_colT), ("s_col", s_col)],
                    stream)
-    _record(stream, [t for t, given in ((q_row, given_q_row), (s_row, given_s_row),
-                                         (q_colT, given_q_colT), (s_col, given_s_col)) if not given])
     _check(lib.fp8_quantize_act_1x128(_ptr(x), rows, cols, int(mode), _ptr(q_row), _ptr(s_row),
                                       _ptr(q_colT), _ptr(s_col), _stream(stream)),
            "fp8_quantize_act_1x128")
@@ -241,6 +255,8 @@ def fp8_swiglu_quantize_1x128(gate_up, mode=BOTH, q_row=None, s_row=None, q_colT
     a bf16 gate_up activation [rows, 2 * ffn] without forming H in memory.
     Returns (q_row, s_row, q_colT, s_col) of H [rows, ffn]; entries of a
     grouping the mode leaves out are None."""
+    if stream is not None:
+        return _elsewhere(fp8_swiglu_quantize_1x128, stream, gate_up, mode, q_row, s_row, q_colT, s_col)
     lib = load()
     if gate_up.dtype != torch.bfloat16 or gate_up.dim() != 2 or gate_up.shape[1] % 2:
         raise TypeError("gate_up must be a 2-D bfloat16 tensor with an even number of columns")
@@ -248,7 +264,6 @@ def fp8_swiglu_quantize_1x128(gate_up, mode=BOTH, q_row=None, s_row=None, q_colT
     ffn = cols2 // 2
     _want(gate_up, torch.bfloat16, (rows, cols2), "gate_up")
     dev = gate_up.device
-    given = [t is not None for t in (q_row, s_row, q_colT, s_col)]
     if mode & ROWWISE:
         q_row = _out(q_row, torch.uint8, (rows, ffn), dev, "q_row")
         s_row = _out(s_row, torch.float32, (ffn // 128, rows), dev, "s_row")
@@ -262,7 +277,6 @@ def fp8_swiglu_quantize_1x128(gate_up, mode=BOTH, q_row=None, s_row=None, q_colT
     outs = (q_row, s_row, q_colT, s_col)
     _launch_checks([("gate_up", gate_up), ("q_row", q_row), ("s_row", s_row), ("q_colT", q_colT),
                     ("s_col", s_col)], stream)
-    _record(stream, [t for t, g in zip(outs, given) if not g])
     _check(lib.fp8_swiglu_quantize_1x128(_ptr(gate_up), rows, ffn, int(mode), _ptr(q_row), _ptr(s_row),
                                          _ptr(q_colT), _ptr(s_col), _stream(stream)),
            "fp8_swiglu_quantize_1x128")
@@ -272,16 +286,15 @@ def fp8_swiglu_quantize_1x128(gate_up, mode=BOTH, q_row=None, s_row=None, q_colT
 def fp8_rmsnorm_rstd(x, eps=1e-6, rstd=None, stream=None):
     """RMSNorm's rstd[i] = 1 / sqrt(mean(x[i]^2) + eps) (float32 [rows]) of a
     bf16 x [rows, cols]."""
+    if stream is not None and rstd is None:
+        return _elsewhere(fp8_rmsnorm_rstd, stream, x, eps, rstd)
     lib = load()
     if x.dtype != torch.bfloat16 or x.dim() != 2:
         raise TypeError("x must be a 2-D bfloat16 tensor")
     rows, cols = x.shape
     _want(x, torch.bfloat16, (rows, cols), "x")
-    given = rstd is not None
     rstd = _out(rstd, torch.float32, (rows,), x.device, "rstd")
     _launch_checks([("x", x), ("rstd", rstd)], stream)
-    if not given:
-        _record(stream, [rstd])
     _check(lib.fp8_rmsnorm_rstd(_ptr(x), rows, cols, float(eps), _ptr(rstd), _stream(stream)), "fp8_rmsnorm_rstd")
     return rstd
 
@@ -292,6 +305,8 @@ def fp8_rmsnorm_quantize_1x128(x, rstd, gamma, mode=BOTH, q_row=None, s_row=None
     float32 [rows], gamma bf16 [cols]) of a bf16 x [rows, cols] without
     forming y in memory.  Returns (q_row, s_row, q_colT, s_col) of y;
     entries of a grouping the mode leaves out are None."""
+    if stream is not None:
+        return _elsewhere(fp8_rmsnorm_quantize_1x128, stream, x, rstd, gamma, mode, q_row, s_row, q_colT, s_col)
     lib = load()
     if x.dtype != torch.bfloat16 or x.dim() != 2:
         raise TypeError("x must be a 2-D bfloat16 tensor")
@@ -300,7 +315,6 @@ def fp8_rmsnorm_quantize_1x128(x, rstd, gamma, mode=BOTH, q_row=None, s_row=None
     _want(rstd, torch.float32, (rows,), "rstd")
     _want(gamma, torch.bfloat16, (cols,), "gamma")
     dev = x.device
-    given = [t is not None for t in (q_row, s_row, q_colT, s_col)]
     if mode & ROWWISE:
         q_row = _out(q_row, torch.uint8, (rows, cols), dev, "q_row")
         s_row = _out(s_row, torch.float32, (cols // 128, rows), dev, "s_row")
@@ -314,7 +328,6 @@ def fp8_rmsnorm_quantize_1x128(x, rstd, gamma, mode=BOTH, q_row=None, s_row=None
     outs = (q_row, s_row, q_colT, s_col)
     _launch_checks([("x", x), ("rstd", rstd), ("gamma", gamma), ("q_row", q_row), ("s_row", s_row),
                     ("q_colT", q_colT), ("s_col", s_col)], stream)
-    _record(stream, [t for t, g in zip(outs, given) if not g])
     _check(lib.fp8_rmsnorm_quantize_1x128(_ptr(x), rows, cols, _ptr(rstd), _ptr(gamma), int(mode), _ptr(q_row),
                                           _ptr(s_row), _ptr(q_colT), _ptr(s_col), _stream(stream)),
            "fp8_rmsnorm_quantize_1x128")
@@ -333,42 +346,32 @@ def _on(t, dtype, shape, dev, name):
     return t
 
 
-def _given(t, dtype, shape, like, dev, new, name):
-    """t checked, or a new tensor noted in `new` (from the cheapest call down)."""
+def _given(t, dtype, shape, like, dev, name):
+    """t checked, or a new tensor (by the cheapest call)."""
     if t is not None:
         return _on(t, dtype, shape, dev, name)
     if like.shape == shape and like.is_contiguous():
-        t = torch.empty_like(like) if like.dtype == dtype else torch.empty_like(like, dtype=dtype)
-    else:
-        t = like.new_empty(shape) if like.dtype == dtype else like.new_empty(shape, dtype=dtype)
-    new.append(t)
-    return t
+        return torch.empty_like(like) if like.dtype == dtype else torch.empty_like(like, dtype=dtype)
+    return like.new_empty(shape) if like.dtype == dtype else like.new_empty(shape, dtype=dtype)
 
 
-def _launch(dev, stream, new):
-    """The stream's handle, once the tensors' device is known to be current."""
+def _current(dev):
+    """The current stream's handle, once the tensors' device is known to be current."""
     if dev != torch.cuda.current_device():
         raise ValueError(f"the tensors are on cuda:{dev} but the current CUDA device is "
                          f"cuda:{torch.cuda.current_device()}; call inside torch.cuda.device({dev})")
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    if not isinstance(stream, torch.cuda.Stream):      # a handle: scratch made here is the call's own to look after
-        stream = torch.cuda.ExternalStream(int(stream), device=dev)
-    _check_devices([], dev, stream)
-    _record(stream, new)
-    return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _scratch(workspace, bytes_, like, dev, new):
-    """(pointer, bytes) of the workspace, allocated when left out."""
+def _scratch(workspace, bytes_, like, dev):
+    """The workspace, allocated when left out, and its bytes."""
     if workspace is None:
         workspace = like.new_empty((bytes_(),), dtype=torch.uint8)
-        new.append(workspace)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         if not workspace.is_cuda or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor")
         _check_devices([("workspace", workspace)], dev)
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def fp8_add_rmsnorm_quantize_1x128(x, gamma, residual=None, eps=1e-6, mode=BOTH, sum_out=None, rstd=None, q_row=None,
@@ -378,8 +381,11 @@ def fp8_add_rmsnorm_quantize_1x128(x, gamma, residual=None, eps=1e-6, mode=BOTH,
     s_row, q_colT, s_col); entries of a grouping the mode leaves out are None,
     and s is x itself without a residual.  sum_out may be x or residual (in
     place)."""
+    if stream is not None:
+        return _elsewhere(fp8_add_rmsnorm_quantize_1x128, stream, x, gamma, residual, eps, mode, sum_out, rstd,
+                          q_row, s_row, q_colT, s_col)
     lib = _lib or load()
-    if stream is None and _host is not None:
+    if _host is not None:
         out = _plain("add_rmsnorm_quantize", "fp8_add_rmsnorm_quantize_1x128", x, gamma, residual, eps, mode, sum_out, rstd,
                      q_row, s_row, q_colT, s_col)
         if out is not None:
@@ -392,24 +398,23 @@ def fp8_add_rmsnorm_quantize_1x128(x, gamma, residual=None, eps=1e-6, mode=BOTH,
     dev = x.get_device()
     _on(x, bf16, shape, dev if dev >= 0 else None, "x")
     _on(gamma, bf16, (cols,), dev, "gamma")
-    new = []
     if residual is not None:
         _on(residual, bf16, shape, dev, "residual")
-        sum_out = _given(sum_out, bf16, shape, x, dev, new, "sum_out")
+        sum_out = _given(sum_out, bf16, shape, x, dev, "sum_out")
     elif sum_out is not None:
         raise ValueError("sum_out needs a residual: without one the sum is x itself")
-    rstd = _given(rstd, f32, (rows,), x, dev, new, "rstd")
+    rstd = _given(rstd, f32, (rows,), x, dev, "rstd")
     if mode & ROWWISE:
-        q_row = _given(q_row, u8, shape, x, dev, new, "q_row")
-        s_row = _given(s_row, f32, (cols // 128, rows), rstd, dev, new, "s_row")
+        q_row = _given(q_row, u8, shape, x, dev, "q_row")
+        s_row = _given(s_row, f32, (cols // 128, rows), rstd, dev, "s_row")
     else:
         q_row = s_row = None
     if mode & COLWISE:
-        q_colT = _given(q_colT, u8, (cols, rows), x, dev, new, "q_colT")
-        s_col = _given(s_col, f32, (rows // 128, cols), rstd, dev, new, "s_col")
+        q_colT = _given(q_colT, u8, (cols, rows), x, dev, "q_colT")
+        s_col = _given(s_col, f32, (rows // 128, cols), rstd, dev, "s_col")
     else:
         q_colT = s_col = None
-    handle = _launch(dev, stream, new)
+    handle = _current(dev)
     st = lib.fp8_add_rmsnorm_quantize_1x128(x.data_ptr(), _ptr(residual), rows, cols, float(eps), gamma.data_ptr(),
                                             int(mode), _ptr(sum_out), rstd.data_ptr(), _ptr(q_row), _ptr(s_row), _ptr(q_colT),
                                             _ptr(s_col), handle)
@@ -434,8 +439,10 @@ def fp8_rmsnorm_backward(dy, s, rstd, gamma, dresidual=None, ds=None, dgamma=Non
     residual path's gradient of s if there is one.  ds (bf16) may be dy or
     dresidual (in place); dgamma is float32 [cols], added to with
     accumulate=True (it must then be given)."""
+    if stream is not None:
+        return _elsewhere(fp8_rmsnorm_backward, stream, dy, s, rstd, gamma, dresidual, ds, dgamma, accumulate, workspace)
     lib = _lib or load()
-    if stream is None and _host is not None:
+    if _host is not None:
         out = _plain("rmsnorm_backward", "fp8_rmsnorm_backward", dy, s, rstd, gamma, dresidual, ds, dgamma, accumulate,
                      workspace)
         if out is not None:
@@ -454,13 +461,13 @@ def fp8_rmsnorm_backward(dy, s, rstd, gamma, dresidual=None, ds=None, dgamma=Non
         _on(dresidual, bf16, shape, dev, "dresidual")
     if accumulate and dgamma is None:
         raise ValueError("accumulate=True needs the dgamma to add to")
-    new = []
-    ds = _given(ds, bf16, shape, s, dev, new, "ds")
-    dgamma = _given(dgamma, f32, (cols,), rstd, dev, new, "dgamma")
-    ws, size = _scratch(workspace, lambda: fp8_rmsnorm_backward_workspace_bytes(rows, cols), s, dev, new)
-    handle = _launch(dev, stream, new)
+    ds = _given(ds, bf16, shape, s, dev, "ds")
+    dgamma = _given(dgamma, f32, (cols,), rstd, dev, "dgamma")
+    workspace, size = _scratch(workspace, lambda: fp8_rmsnorm_backward_workspace_bytes(rows, cols), s, dev)
+    handle = _current(dev)
     st = lib.fp8_rmsnorm_backward(dy.data_ptr(), s.data_ptr(), rstd.data_ptr(), gamma.data_ptr(), _ptr(dresidual), rows,
-                                  cols, ds.data_ptr(), dgamma.data_ptr(), 1 if accumulate else 0, ws, size, handle)
+                                  cols, ds.data_ptr(), dgamma.data_ptr(), 1 if accumulate else 0,
+                                  workspace.data_ptr(), size, handle)
     if st:
         raise Fp8Error(st, "fp8_rmsnorm_backward")
     return ds, dgamma
@@ -497,8 +504,11 @@ def fp8_token_logprobs(logits, targets=None, topk=0, logprob=None, entropy=None,
     by index) of bf16 or float32 logits [rows, vocab].  Returns (logprob,
     entropy, stats, top_logprob, top_index); logprob is None without targets,
     the last two with topk = 0."""
+    if stream is not None:
+        return _elsewhere(fp8_token_logprobs, stream, logits, targets, topk, logprob, entropy, stats, top_logprob,
+                          top_index)
     lib = _lib or load()
-    if stream is None and _host is not None:
+    if _host is not None:
         out = _plain("token_logprobs", "fp8_token_logprobs", logits, targets, topk, logprob, entropy, stats, top_logprob,
                      top_index)
         if out is not None:
@@ -507,20 +517,19 @@ def fp8_token_logprobs(logits, targets=None, topk=0, logprob=None, entropy=None,
     code, ld = _logits(logits, "logits")
     rows, vocab = logits.shape
     dev = logits.get_device()
-    new = []
-    entropy = _given(entropy, f32, (rows,), logits, dev, new, "entropy")
+    entropy = _given(entropy, f32, (rows,), logits, dev, "entropy")
     if targets is not None:
         _on(targets, i64, (rows,), dev, "targets")
-        logprob = _given(logprob, f32, (rows,), entropy, dev, new, "logprob")
+        logprob = _given(logprob, f32, (rows,), entropy, dev, "logprob")
     else:
         logprob = None
-    stats = _given(stats, f32, (rows, 2), entropy, dev, new, "stats")
+    stats = _given(stats, f32, (rows, 2), entropy, dev, "stats")
     if topk > 0:
-        top_logprob = _given(top_logprob, f32, (rows, topk), entropy, dev, new, "top_logprob")
-        top_index = _given(top_index, i64, (rows, topk), top_logprob, dev, new, "top_index")
+        top_logprob = _given(top_logprob, f32, (rows, topk), entropy, dev, "top_logprob")
+        top_index = _given(top_index, i64, (rows, topk), top_logprob, dev, "top_index")
     else:
         top_logprob = top_index = None
-    handle = _launch(dev, stream, new)
+    handle = _current(dev)
     st = lib.fp8_token_logprobs(logits.data_ptr(), code, rows, vocab, ld, _ptr(targets), int(topk), _ptr(logprob),
                                 entropy.data_ptr(), stats.data_ptr(), _ptr(top_logprob), _ptr(top_index), handle)
     if st:
@@ -533,8 +542,11 @@ def fp8_token_logprobs_backward(logits, targets, stats, dlogprob=None, entropy=N
     """Gradient of the logits from the gradients of fp8_token_logprobs's
     logprob and entropy (float32 [rows], either None); entropy is needed with
     dentropy.  dlogits (the logits' type) may be the logits themselves."""
+    if stream is not None:
+        return _elsewhere(fp8_token_logprobs_backward, stream, logits, targets, stats, dlogprob, entropy, dentropy,
+                          dlogits)
     lib = _lib or load()
-    if stream is None and _host is not None:
+    if _host is not None:
         out = _plain("token_logprobs_backward", "fp8_token_logprobs_backward", logits, targets, stats, dlogprob, entropy,
                      dentropy, dlogits)
         if out is not None:
@@ -555,14 +567,13 @@ def fp8_token_logprobs_backward(logits, targets, stats, dlogprob=None, entropy=N
             raise ValueError("dentropy needs the entropy")
         _on(dentropy, f32, (rows,), dev, "dentropy")
         _on(entropy, f32, (rows,), dev, "entropy")
-    new = []
     if dlogits is None:
-        dlogits = _given(None, logits.dtype, (rows, vocab), logits, dev, new, "dlogits")
+        dlogits = _given(None, logits.dtype, (rows, vocab), logits, dev, "dlogits")
         ld_out = vocab
     else:
         _, ld_out = _logits(dlogits, "dlogits", logits)
         _check_devices([("dlogits", dlogits)], dev)
-    handle = _launch(dev, stream, new)
+    handle = _current(dev)
     st = lib.fp8_token_logprobs_backward(logits.data_ptr(), code, rows, vocab, ld, _ptr(targets), stats.data_ptr(),
                                          _ptr(dlogprob), _ptr(entropy), _ptr(dentropy), dlogits.data_ptr(), ld_out,
                                          handle)
@@ -584,6 +595,8 @@ def fp8_newton_schulz(g, coefficients=NEWTON_SCHULZ_COEFFICIENTS, eps=1e-7, out=
     [batch, m, n], bf16 or float32), one step per (a, b, c) of coefficients.
     Returns a bf16 tensor of g's shape.  workspace: optional uint8 scratch of
     fp8_newton_schulz_workspace_bytes (allocated when left out)."""
+    if stream is not None:
+        return _elsewhere(fp8_newton_schulz, stream, g, coefficients, eps, out, workspace)
     lib = _lib or load()
     if g.dim() not in (2, 3) or g.dtype not in _DTYPES:
         raise TypeError("g must be a 2-D or 3-D bfloat16 or float32 tensor")
@@ -595,12 +608,11 @@ def fp8_newton_schulz(g, coefficients=NEWTON_SCHULZ_COEFFICIENTS, eps=1e-7, out=
     if any(len(step) != 3 for step in coefficients):
         raise ValueError("each step takes three coefficients")
     table = (ctypes.c_float * (3 * steps))(*[float(v) for step in coefficients for v in step])
-    new = []
-    out = _given(out, torch.bfloat16, shape, g, dev, new, "out")
-    ws, size = _scratch(workspace, lambda: fp8_newton_schulz_workspace_bytes(batch, m, n), g, dev, new)
-    handle = _launch(dev, stream, new)
+    out = _given(out, torch.bfloat16, shape, g, dev, "out")
+    workspace, size = _scratch(workspace, lambda: fp8_newton_schulz_workspace_bytes(batch, m, n), g, dev)
+    handle = _current(dev)
     _check(lib.fp8_newton_schulz(g.data_ptr(), _DTYPES[g.dtype], batch, m, n, ctypes.cast(table, ctypes.c_void_p),
-                                 steps, float(eps), out.data_ptr(), ws, size, handle),
+                                 steps, float(eps), out.data_ptr(), workspace.data_ptr(), size, handle),
            "fp8_newton_schulz")
     return out
 
@@ -608,18 +620,18 @@ def fp8_newton_schulz(g, coefficients=NEWTON_SCHULZ_COEFFICIENTS, eps=1e-7, out=
 def fp8_quantize_weight_128x128(w, wq=None, sw=None, wqT=None, transposed=True, stream=None):
     """Quantize a bf16 weight [n, k] in 128x128 blocks.  Returns (wq, sw, wqT);
     wqT is None when transposed is False and no buffer is passed."""
+    if stream is not None:
+        return _elsewhere(fp8_quantize_weight_128x128, stream, w, wq, sw, wqT, transposed)
     lib = load()
     if w.dtype != torch.bfloat16 or w.dim() != 2:
         raise TypeError("w must be a 2-D bfloat16 tensor")
     n, k = w.shape
     _want(w, torch.bfloat16, (n, k), "w")
-    allocated = [t is None for t in (wq, sw, wqT)]
     wq = _out(wq, torch.uint8, (n, k), w.device, "wq")
     sw = _out(sw, torch.float32, (n // 128, k // 128), w.device, "sw")
     if wqT is not None or transposed:
         wqT = _out(wqT, torch.uint8, (k, n), w.device, "wqT")
     _launch_checks([("w", w), ("wq", wq), ("sw", sw), ("wqT", wqT)], stream)
-    _record(stream, [t for t, a in zip((wq, sw, wqT), allocated) if a])
     _check(lib.fp8_quantize_weight_128x128(_ptr(w), n, k, _ptr(wq), _ptr(sw), _ptr(wqT),
                                            _stream(stream)),
            "fp8_quantize_weight_128x128")
@@ -656,6 +668,8 @@ def fp8_block_gemm_fprop(xq, sx, wq, sw, y=None, stream=None, workspace=None):
     """Y[M, N] = X W^T (bf16) from X codes [M, K] / scales [K/128, M] and W
     codes [N, K] / scales [N/128, K/128].  workspace: optional (see
     fp8_gemm_workspace)."""
+    if stream is not None and y is None:
+        return _elsewhere(fp8_block_gemm_fprop, stream, xq, sx, wq, sw, y, workspace=workspace)
     lib = load()
     M, K = xq.shape
     N = wq.shape[0]
@@ -663,11 +677,9 @@ def fp8_block_gemm_fprop(xq, sx, wq, sw, y=None, stream=None, workspace=None):
     _want(sx, torch.float32, (K // 128, M), "sx")
     _want(wq, torch.uint8, (N, K), "wq")
     _want(sw, torch.float32, (N // 128, K // 128), "sw")
-    allocated = y is None
     y = _out(y, torch.bfloat16, (M, N), xq.device, "y")
     _launch_checks([("xq", xq), ("sx", sx), ("wq", wq), ("sw", sw), ("y", y), ("workspace", workspace)],
                    stream)
-    _record(stream, [y] if allocated else [])
     _check(lib.fp8_block_gemm_fprop(_ptr(xq), _ptr(sx), _ptr(wq), _ptr(sw), _ptr(y), M, N, K,
                                     *_workspace(workspace), _stream(stream)),
            "fp8_block_gemm_fprop")
@@ -677,6 +689,8 @@ def fp8_block_gemm_fprop(xq, sx, wq, sw, y=None, stream=None, workspace=None):
 def fp8_block_gemm_dgrad(dyq, sdy, wqT, sw, dx=None, stream=None, workspace=None):
     """dX[M, K] = dY W (bf16) from dY codes [M, N] / scales [N/128, M], the
     transposed weight codes [K, N] and the weight scales [N/128, K/128]."""
+    if stream is not None and dx is None:
+        return _elsewhere(fp8_block_gemm_dgrad, stream, dyq, sdy, wqT, sw, dx, workspace=workspace)
     lib = load()
     M, N = dyq.shape
     K = wqT.shape[0]
@@ -684,11 +698,9 @@ def fp8_block_gemm_dgrad(dyq, sdy, wqT, sw, dx=None, stream=None, workspace=None
     _want(sdy, torch.float32, (N // 128, M), "sdy")
     _want(wqT, torch.uint8, (K, N), "wqT")
     _want(sw, torch.float32, (N // 128, K // 128), "sw")
-    allocated = dx is None
     dx = _out(dx, torch.bfloat16, (M, K), dyq.device, "dx")
     _launch_checks([("dyq", dyq), ("sdy", sdy), ("wqT", wqT), ("sw", sw), ("dx", dx),
                     ("workspace", workspace)], stream)
-    _record(stream, [dx] if allocated else [])
     _check(lib.fp8_block_gemm_dgrad(_ptr(dyq), _ptr(sdy), _ptr(wqT), _ptr(sw), _ptr(dx), M, N, K,
                                     *_workspace(workspace), _stream(stream)),
            "fp8_block_gemm_dgrad")
@@ -698,6 +710,8 @@ def fp8_block_gemm_dgrad(dyq, sdy, wqT, sw, dx=None, stream=None, workspace=None
 def fp8_block_gemm_wgrad(dyqT, sdyT, xqT, sxT, dw=None, stream=None, workspace=None):
     """dW[N, K] = dY^T X (bf16) from along-token codes: dY^T [N, M] / scales
     [M/128, N] and X^T [K, M] / scales [M/128, K]."""
+    if stream is not None and dw is None:
+        return _elsewhere(fp8_block_gemm_wgrad, stream, dyqT, sdyT, xqT, sxT, dw, workspace=workspace)
     lib = load()
     N, M = dyqT.shape
     K = xqT.shape[0]
@@ -705,11 +719,9 @@ def fp8_block_gemm_wgrad(dyqT, sdyT, xqT, sxT, dw=None, stream=None, workspace=N
     _want(sdyT, torch.float32, (M // 128, N), "sdyT")
     _want(xqT, torch.uint8, (K, M), "xqT")
     _want(sxT, torch.float32, (M // 128, K), "sxT")
-    allocated = dw is None
     dw = _out(dw, torch.bfloat16, (N, K), dyqT.device, "dw")
     _launch_checks([("dyqT", dyqT), ("sdyT", sdyT), ("xqT", xqT), ("sxT", sxT), ("dw", dw),
                     ("workspace", workspace)], stream)
-    _record(stream, [dw] if allocated else [])
     _check(lib.fp8_block_gemm_wgrad(_ptr(dyqT), _ptr(sdyT), _ptr(xqT), _ptr(sxT), _ptr(dw), N, K, M,
                                     *_workspace(workspace), _stream(stream)),
            "fp8_block_gemm_wgrad")
@@ -792,6 +804,8 @@ def fp8_block_gemm_wgrad_static_ws(dyqT, sdyT, xqT, sxT, dw=None, stream=None):
     """dW = dY^T X (bf16) like fp8_block_gemm_wgrad, with the split
     schedule's workspace inside the library (no device buffer passed), for
     callers that cannot allocate one; calls must not overlap on the GPU."""
+    if stream is not None and dw is None:
+        return _elsewhere(fp8_block_gemm_wgrad_static_ws, stream, dyqT, sdyT, xqT, sxT, dw)
     lib = load()
     N, M = dyqT.shape
     K = xqT.shape[0]
@@ -799,10 +813,8 @@ def fp8_block_gemm_wgrad_static_ws(dyqT, sdyT, xqT, sxT, dw=None, stream=None):
     _want(sdyT, torch.float32, (M // 128, N), "sdyT")
     _want(xqT, torch.uint8, (K, M), "xqT")
     _want(sxT, torch.float32, (M // 128, K), "sxT")
-    allocated = dw is None
     dw = _out(dw, torch.bfloat16, (N, K), dyqT.device, "dw")
     _launch_checks([("dyqT", dyqT), ("sdyT", sdyT), ("xqT", xqT), ("sxT", sxT), ("dw", dw)], stream)
-    _record(stream, [dw] if allocated else [])
     _check(lib.fp8_block_gemm_wgrad_static_ws(_ptr(dyqT), _ptr(sdyT), _ptr(xqT), _ptr(sxT), _ptr(dw), N, K, M,
                                               _stream(stream)),
            "fp8_block_gemm_wgrad_static_ws")
@@ -837,13 +849,13 @@ def fp8_last_cuda_error() -> str:
 
 
 def fp8_cast_e4m3_scaled(x, scale: float, q=None, stream=None):
+    if stream is not None and q is None:
+        return _elsewhere(fp8_cast_e4m3_scaled, stream, x, scale, q)
     lib = load()
     n = x.numel()
     _want(x, torch.float32, tuple(x.shape), "x")
-    allocated = q is None
     q = _out(q, torch.uint8, tuple(x.shape), x.device, "q")
     _launch_checks([("x", x), ("q", q)], stream)
-    _record(stream, [q] if allocated else [])
     _check(lib.fp8_cast_e4m3_scaled(_ptr(x), ctypes.c_float(scale), _ptr(q), n, _stream(stream)),
            "fp8_cast_e4m3_scaled")
     return q
@@ -853,6 +865,8 @@ def fp8_selftest_division(stream=None):
     """Returns (code mismatches, first code mismatch, quotient-bit
     mismatches with |x/s| >= 2^-12, first such, quotient-bit mismatches
     below 2^-12)."""
+    if stream is not None:
+        return _elsewhere(fp8_selftest_division, stream)
     res = torch.zeros(6, dtype=torch.int64, device="cuda")
     _check(load().fp8_selftest_division(_ptr(res), _stream(stream)), "fp8_selftest_division")
     torch.cuda.synchronize()
@@ -873,6 +887,8 @@ def fp8_selftest_silu_bf16(stream=None):
     """silu of every bfloat16 bit pattern as the fused SwiGLU producer
     computes it: a numpy uint16 array of 65536 bit patterns (index = input
     bits)."""
+    if stream is not None:
+        return _elsewhere(fp8_selftest_silu_bf16, stream)
     out = torch.empty(65536, dtype=torch.int16, device="cuda")
     _check(load().fp8_selftest_silu_bf16(_ptr(out), _stream(stream)), "fp8_selftest_silu_bf16")
     torch.cuda.synchronize()

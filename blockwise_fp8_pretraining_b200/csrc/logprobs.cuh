@@ -7,7 +7,8 @@
 //   H       = -sum_v p_v logp_v = L - (sum_v exp(d_v) d_v) / sum_v exp(d_v)
 //   dx_v    = g (1[v = target] - p_v) - h p_v (logp_v + H)
 //
-// for the gradients g of the target's log probability and h of the entropy.
+// for the gradients g of the target's log probability and h of the entropy.  (1 -
+// p of the target itself is -expm1(logp), which keeps its digits when p is near 1.)
 //
 // Everything is referred to the row's maximum: rows of the type's lowest value,
 // or of huge values, come out right, and neither L nor H subtracts large
@@ -41,7 +42,7 @@
 // TB/s; [1024, 151936] FP32 92 us, 6.7 TB/s), a few rows by the latency of one
 // load and the joins (one row 5.3 us).  Alternatives add the insertions: 20 of them
 // 294 us on [4096, 151936], 10.7 us on one row.  The gradient reads and writes at
-// 6.65 TB/s ([4096, 151936] bf16 374 us).
+// 6.7 TB/s ([4096, 151936] bf16 371 us).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -611,8 +612,7 @@ __global__ void __launch_bounds__(kMaxThreads, 2)
 // blockIdx.x = row * chunks + chunk; a chunk is blockDim.x * kBatch vectors of
 // the row (the first also takes the elements before the first 16-byte
 // boundary, the last those after the last).  dlogits may be logits itself:
-// every element is read and then written by one thread (the target's own
-// logit is an element like any other).
+// every element is read and then written by one thread.
 // ENT: with the entropy's gradient.
 template <typename T, bool ENT>
 __global__ void __launch_bounds__(kMaxThreads, 3)
@@ -644,7 +644,7 @@ __global__ void __launch_bounds__(kMaxThreads, 3)
     const float h = ENT ? __ldg(dentropy + row) : 0.0f;
     const float H = ENT ? __ldg(entropy + row) : 0.0f;
 
-    // without the target's own + g
+    // an element that is not the target
     auto grad2 = [&](float& a, float& b) {
         float2 lp = __fadd2_rn(__fadd2_rn(make_float2(a, b), make_float2(nm, nm)), make_float2(-st.y, -st.y));
         if (ENT) {                     // (0 * -inf would be NaN)
@@ -661,11 +661,33 @@ __global__ void __launch_bounds__(kMaxThreads, 3)
     auto single = [&](int64_t at) {
         float f = E::load(x + at), unused = 0.0f;
         grad2(f, unused);
-        E::store(out + at, at == target ? f + g : f);
+        E::store(out + at, f);
     };
-    // the target's vector and place in it (no vector: head, tail or no target)
-    const int64_t tv = target >= head && target < tail0 ? (target - head) / E::N : -1;
-    const int tj = static_cast<int>((target - head) % E::N);
+    // The target's element is stored a second time, by the thread that has it (and
+    // read ahead, as out may be x).
+    bool mine;
+    if (target < head) {
+        mine = chunk == 0 && target == threadIdx.x;
+    } else if (target < tail0) {
+        const int64_t d = (target - head) / E::N - i0;
+        mine = d >= 0 && d < static_cast<int64_t>(blockDim.x) * kBatch && (d & (blockDim.x - 1)) == 0;
+    } else {
+        mine = chunk == chunks - 1 && target == tail0 + threadIdx.x && target < vocab;
+    }
+    float hit = 0.0f;
+    if (mine) {
+        // g (1 - p) of a likely target from log p: g - g p would lose its digits
+        float unused = 0.0f;
+        hit = E::load(x + target);
+        const float lp = (hit + nm) - st.y;
+        grad2(hit, unused);
+        if (lp > -kLn2) {
+            hit = -g * expm1f(lp);
+            if (ENT) hit = fmaf(-h * ex2(lp * kLog2e), lp + H, hit);
+        } else {                       // (NaN among them)
+            hit += g;
+        }
+    }
     const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
@@ -676,11 +698,6 @@ __global__ void __launch_bounds__(kMaxThreads, 3)
             const int64_t at = head + i * E::N;
 #pragma unroll
             for (int j = 0; j < E::N; j += 2) grad2(f[j], f[j + 1]);
-            if (i == tv) {
-#pragma unroll
-                for (int j = 0; j < E::N; ++j)
-                    if (j == tj) f[j] += g;
-            }
             if (same) {
                 *reinterpret_cast<uint4*>(out + at) = E::pack(f);
             } else {
@@ -691,6 +708,7 @@ __global__ void __launch_bounds__(kMaxThreads, 3)
     }
     if (chunk == 0 && threadIdx.x < head) single(threadIdx.x);
     if (chunk == chunks - 1 && threadIdx.x < vocab - tail0) single(tail0 + threadIdx.x);
+    if (mine) E::store(out + target, hit);
 }
 
 }  // namespace logp

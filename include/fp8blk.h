@@ -321,7 +321,8 @@ fp8_status fp8_token_logprobs(const void *logits, int dtype, int64_t rows, int64
 /*
  * Gradient of the logits: with p = exp(x - m - L) from stats,
  *   dlogits_v = dlogprob (1[v = target] - p_v) - dentropy p_v (log p_v + entropy)
- * in FP32, rounded once to the logits' type.  A row without a target (negative)
+ * in FP32 (the target's 1 - p from log p, so that a likely one keeps its digits),
+ * rounded once to the logits' type.  A row without a target (negative)
  * takes no part of dlogprob; a target >= vocab makes the row NaN.
  *
  *   logits, dtype, rows, vocab, ld, targets: as fp8_token_logprobs; targets may

@@ -355,6 +355,24 @@ def _given(t, dtype, shape, like, dev, name):
     return like.new_empty(shape) if like.dtype == dtype else like.new_empty(shape, dtype=dtype)
 
 
+def _aligned(t):
+    """t, or a copy on the current stream where t (a slice of a longer tensor) does
+    not begin at a multiple of 16 bytes, as the library has it."""
+    return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _aside(outputs):
+    """Where the library may write the outputs: themselves, or a new tensor in the
+    place of one that does not begin at a multiple of 16 bytes."""
+    return [t if t is None or t.data_ptr() % 16 == 0 else torch.empty_like(t) for t in outputs]
+
+
+def _bring(outputs, written):
+    for t, w in zip(outputs, written):
+        if w is not t:
+            t.copy_(w)
+
+
 def _current(dev):
     """The current stream's handle, once the tensors' device is known to be current."""
     if dev != torch.cuda.current_device():
@@ -455,7 +473,7 @@ def fp8_rmsnorm_backward(dy, s, rstd, gamma, dresidual=None, ds=None, dgamma=Non
     dev = s.get_device()
     _on(s, bf16, shape, dev if dev >= 0 else None, "s")
     _on(dy, bf16, shape, dev, "dy")
-    _on(rstd, f32, (rows,), dev, "rstd")
+    rstd = _aligned(_on(rstd, f32, (rows,), dev, "rstd"))
     _on(gamma, bf16, (cols,), dev, "gamma")
     if dresidual is not None:
         _on(dresidual, bf16, shape, dev, "dresidual")
@@ -503,7 +521,8 @@ def fp8_token_logprobs(logits, targets=None, topk=0, logprob=None, entropy=None,
     probabilities and int64 indices [rows, topk], largest first, equal logits
     by index) of bf16 or float32 logits [rows, vocab].  Returns (logprob,
     entropy, stats, top_logprob, top_index); logprob is None without targets,
-    the last two with topk = 0."""
+    the last two with topk = 0.  Per-row arguments may be slices of longer tensors
+    (one that does not begin at a multiple of 16 bytes is copied)."""
     if stream is not None:
         return _elsewhere(fp8_token_logprobs, stream, logits, targets, topk, logprob, entropy, stats, top_logprob,
                           top_index)
@@ -519,7 +538,7 @@ def fp8_token_logprobs(logits, targets=None, topk=0, logprob=None, entropy=None,
     dev = logits.get_device()
     entropy = _given(entropy, f32, (rows,), logits, dev, "entropy")
     if targets is not None:
-        _on(targets, i64, (rows,), dev, "targets")
+        targets = _aligned(_on(targets, i64, (rows,), dev, "targets"))
         logprob = _given(logprob, f32, (rows,), entropy, dev, "logprob")
     else:
         logprob = None
@@ -530,18 +549,22 @@ def fp8_token_logprobs(logits, targets=None, topk=0, logprob=None, entropy=None,
     else:
         top_logprob = top_index = None
     handle = _current(dev)
-    st = lib.fp8_token_logprobs(logits.data_ptr(), code, rows, vocab, ld, _ptr(targets), int(topk), _ptr(logprob),
-                                entropy.data_ptr(), stats.data_ptr(), _ptr(top_logprob), _ptr(top_index), handle)
+    out = (logprob, entropy, stats, top_logprob, top_index)
+    written = _aside(out)
+    st = lib.fp8_token_logprobs(logits.data_ptr(), code, rows, vocab, ld, _ptr(targets), int(topk), *map(_ptr, written),
+                                handle)
     if st:
         raise Fp8Error(st, "fp8_token_logprobs")
-    return logprob, entropy, stats, top_logprob, top_index
+    _bring(out, written)
+    return out
 
 
 def fp8_token_logprobs_backward(logits, targets, stats, dlogprob=None, entropy=None, dentropy=None, dlogits=None,
                                 stream=None):
     """Gradient of the logits from the gradients of fp8_token_logprobs's
     logprob and entropy (float32 [rows], either None); entropy is needed with
-    dentropy.  dlogits (the logits' type) may be the logits themselves."""
+    dentropy.  dlogits (the logits' type) may be the logits themselves.  Per-row
+    arguments may be slices, as in fp8_token_logprobs."""
     if stream is not None:
         return _elsewhere(fp8_token_logprobs_backward, stream, logits, targets, stats, dlogprob, entropy, dentropy,
                           dlogits)
@@ -555,18 +578,18 @@ def fp8_token_logprobs_backward(logits, targets, stats, dlogprob=None, entropy=N
     code, ld = _logits(logits, "logits")
     rows, vocab = logits.shape
     dev = logits.get_device()
-    _on(stats, f32, (rows, 2), dev, "stats")
+    stats = _aligned(_on(stats, f32, (rows, 2), dev, "stats"))
     if dlogprob is not None:
         if targets is None:
             raise ValueError("dlogprob needs targets")
-        _on(dlogprob, f32, (rows,), dev, "dlogprob")
+        dlogprob = _aligned(_on(dlogprob, f32, (rows,), dev, "dlogprob"))
     if targets is not None:
-        _on(targets, torch.int64, (rows,), dev, "targets")
+        targets = _aligned(_on(targets, torch.int64, (rows,), dev, "targets"))
     if dentropy is not None:
         if entropy is None:
             raise ValueError("dentropy needs the entropy")
-        _on(dentropy, f32, (rows,), dev, "dentropy")
-        _on(entropy, f32, (rows,), dev, "entropy")
+        dentropy = _aligned(_on(dentropy, f32, (rows,), dev, "dentropy"))
+        entropy = _aligned(_on(entropy, f32, (rows,), dev, "entropy"))
     if dlogits is None:
         dlogits = _given(None, logits.dtype, (rows, vocab), logits, dev, "dlogits")
         ld_out = vocab
@@ -608,12 +631,15 @@ def fp8_newton_schulz(g, coefficients=NEWTON_SCHULZ_COEFFICIENTS, eps=1e-7, out=
     if any(len(step) != 3 for step in coefficients):
         raise ValueError("each step takes three coefficients")
     table = (ctypes.c_float * (3 * steps))(*[float(v) for step in coefficients for v in step])
+    g = _aligned(g)
     out = _given(out, torch.bfloat16, shape, g, dev, "out")
+    written, = _aside((out,))
     workspace, size = _scratch(workspace, lambda: fp8_newton_schulz_workspace_bytes(batch, m, n), g, dev)
     handle = _current(dev)
     _check(lib.fp8_newton_schulz(g.data_ptr(), _DTYPES[g.dtype], batch, m, n, ctypes.cast(table, ctypes.c_void_p),
-                                 steps, float(eps), out.data_ptr(), workspace.data_ptr(), size, handle),
+                                 steps, float(eps), written.data_ptr(), workspace.data_ptr(), size, handle),
            "fp8_newton_schulz")
+    _bring((out,), (written,))
     return out
 
 

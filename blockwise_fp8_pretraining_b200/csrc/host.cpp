@@ -57,7 +57,8 @@ struct Call {
         return t;
     }
     bool fits(const Tensor& t, ScalarType type, Shape shape) const {
-        return t.is_cuda() && t.get_device() == dev && t.scalar_type() == type && t.sizes() == shape && t.is_contiguous();
+        return t.is_cuda() && t.get_device() == dev && t.scalar_type() == type && t.sizes() == shape && t.is_contiguous() &&
+               (reinterpret_cast<uintptr_t>(t.data_ptr()) & 15u) == 0;     // (a slice that is not: the binding copies it)
     }
     // the data of a tensor that must be there, or may be None
     void* in(int i, ScalarType type, Shape shape, bool optional = false) {

@@ -16,6 +16,7 @@ import importlib.machinery
 import importlib.util
 import os
 import re
+import warnings
 
 import torch
 
@@ -110,12 +111,17 @@ def load() -> ctypes.CDLL:
 
 
 def _load_host(lib) -> None:
+    """The compiled host side, if it is there and fits the running torch."""
     global _host
     if not os.path.exists(_build.HOST_LIB):
         return
     loader = importlib.machinery.ExtensionFileLoader("_fp8blk_host", _build.HOST_LIB)
-    module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fp8blk_host", loader))
-    loader.exec_module(module)
+    try:
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_fp8blk_host", loader))
+        loader.exec_module(module)
+    except ImportError as e:
+        warnings.warn(f"the binding's compiled host side does not load, its Python one serves: {e}", RuntimeWarning)
+        return
     module.bind(*(ctypes.cast(fn, ctypes.c_void_p).value for fn in (
         lib.fp8_add_rmsnorm_quantize_1x128, lib.fp8_rmsnorm_backward, lib.fp8_rmsnorm_backward_workspace_bytes,
         lib.fp8_token_logprobs, lib.fp8_token_logprobs_backward)))

@@ -576,6 +576,13 @@ NsLayout ns_layout(int64_t batch, int64_t m, int64_t n) {
     return w;
 }
 
+// What a call has to bring.  Where one launch takes the batch it uses none of it;
+// a page all the same, so that a workspace is never NULL.
+constexpr size_t kNsLeastWorkspace = 4096;
+size_t ns_workspace(int64_t batch, int64_t m, int64_t n) {
+    return ns::small::always_takes(batch, m, n) ? kNsLeastWorkspace : ns_layout(batch, m, n).bytes;
+}
+
 // [batch][rows][cols] 16-bit row-major matrices with rows of ld elements.
 fp8_status make_map_3d(CUtensorMap* map, const void* base, int64_t cols, int64_t rows, int64_t batch, int64_t ld,
                        uint32_t box_x, uint32_t box_y, CUtensorMapSwizzle swizzle) {
@@ -713,7 +720,7 @@ fp8_status ns_small_plan(int dev, int sms, int64_t batch, int s, int l, int* ran
     const fp8_status ready = ns_small_ready<T>(dev);
     if (ready != FP8_OK) return ready;
     int64_t best = 0, room = 0;
-    for (int columns = 128; columns <= 256; columns *= 2) {
+    for (int columns = ns::small::kLeastShare; columns <= 2 * ns::small::kLeastShare; columns *= 2) {
         int r = (l + columns - 1) / columns;
         if (r > ns::small::kMaxRanks) r = ns::small::kMaxRanks;
         const int each = ns::small::up16((l + r - 1) / r);
@@ -728,7 +735,7 @@ fp8_status ns_small_plan(int dev, int sms, int64_t batch, int s, int l, int* ran
         *ranks = r;
         *share = each;
     }
-    const bool short_last = s > 80 && *ranks > 1 && best > 1 && 4 * batch < 3 * room;
+    const bool short_last = s > ns::small::kMaxShortOfAnyBatch && *ranks > 1 && best > 1 && 4 * batch < 3 * room;
     const bool many = s > 96 && *ranks > 2 && best > 1 && batch > 48;
     if (short_last || many) *share = 0;
     return FP8_OK;
@@ -1010,7 +1017,7 @@ fp8_status fp8_newton_schulz_workspace_bytes(int64_t batch, int64_t m, int64_t n
     if (!bytes) return FP8_ERR_NULL;
     if (batch < 0 || m < 1 || n < 1 || batch > FP8_NS_MAX_BATCH || m > ns::kMaxSide || n > ns::kMaxSide)
         return FP8_ERR_SHAPE;
-    *bytes = batch ? ns_layout(batch, m, n).bytes : 0;
+    *bytes = batch ? ns_workspace(batch, m, n) : 0;
     return FP8_OK;
 }
 
@@ -1027,21 +1034,12 @@ fp8_status fp8_newton_schulz(const void* g, int dtype, int64_t batch, int64_t m,
     if (batch == 0) return FP8_OK;
     if (!g || !out_bf16 || !workspace) return FP8_ERR_NULL;
     if (!aligned16(g) || !aligned16(out_bf16) || !aligned16(workspace)) return FP8_ERR_ALIGN;
-    const NsLayout w = ns_layout(batch, m, n);
-    if (workspace_bytes < w.bytes) return FP8_ERR_SHAPE;
+    if (workspace_bytes < ns_workspace(batch, m, n)) return FP8_ERR_SHAPE;
     int dev = 0, sms = 0;
     fp8_status st = current_device(&dev);
     if (st != FP8_OK) return st;
     if ((st = sm_count(dev, &sms)) != FP8_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    __half *x[2], *lo[2];
-    for (int i = 0; i < 2; ++i) {
-        x[i] = reinterpret_cast<__half*>(ws + w.x[i]);
-        lo[i] = reinterpret_cast<__half*>(ws + w.lo[i]);
-    }
-    __half* gram = reinterpret_cast<__half*>(ws + w.gram);
-    __half* poly = reinterpret_cast<__half*>(ws + w.poly);
 
     // X is kept times the power of two at or below sqrt(m n), at most 2^13
     // (entries of X up to 8 then stay inside FP16's range).
@@ -1059,6 +1057,16 @@ fp8_status fp8_newton_schulz(const void* g, int dtype, int64_t batch, int64_t m,
                        : launch_ns_small<__nv_bfloat16>(g, batch, m, n, coefficients, steps, eps, scale, out_bf16, ranks,
                                                         share, s);
     }
+    const NsLayout w = ns_layout(batch, m, n);
+    if (workspace_bytes < w.bytes) return FP8_ERR_SHAPE;         // (a page was enough only for one launch)
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    __half *x[2], *lo[2];
+    for (int i = 0; i < 2; ++i) {
+        x[i] = reinterpret_cast<__half*>(ws + w.x[i]);
+        lo[i] = reinterpret_cast<__half*>(ws + w.lo[i]);
+    }
+    __half* gram = reinterpret_cast<__half*>(ws + w.gram);
+    __half* poly = reinterpret_cast<__half*>(ws + w.poly);
     double* partial = reinterpret_cast<double*>(ws + w.partial);
     int* flags = reinterpret_cast<int*>(ws + w.flags);
     const int num_flags = w.slots * 2 * ns::EPI_WARPS;

@@ -37,6 +37,8 @@ constexpr int kMaxShort = 128, kMaxLong = 8192, kMaxRanks = 8;
 constexpr int kTiles = 4;                         // of 16 x 16, a warp's piece of a product at a time
 constexpr int kThreads = 512;
 constexpr int kMaxSteps = 32;
+constexpr int kMaxShortOfAnyBatch = 80;           // up to here one launch takes any batch
+constexpr int kLeastShare = 128;                  // columns of X per CTA, at least (where there are as many)
 
 struct Params {
     int m, n;                   // the matrix as it lies in memory
@@ -68,6 +70,14 @@ inline bool takes(int64_t m, int64_t n) {
     const int64_t s = m < n ? m : n, l = m < n ? n : m;
     return s <= kMaxShort && l <= kMaxLong &&
            smem_bytes(static_cast<int>(s), up16(static_cast<int>(l + kMaxRanks - 1) / kMaxRanks)) <= kMaxSmem;
+}
+
+// Whether a batch takes one launch whatever the number of clusters that run at
+// once (the exceptions concern matrices of several CTAs, of more than 80 rows, in
+// more than one round).
+inline bool always_takes(int64_t batch, int64_t m, int64_t n) {
+    const int64_t s = m < n ? m : n, l = m < n ? n : m;
+    return takes(m, n) && (batch == 1 || s <= kMaxShortOfAnyBatch || l <= kLeastShare);
 }
 
 template <bool TRANS>

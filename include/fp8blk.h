@@ -375,8 +375,9 @@ fp8_status fp8_token_logprobs_backward(const void *logits, int dtype, int64_t ro
  *   eps     >= 0, finite.
  *   out_bf16 [batch, m, n], written; must not overlap g or the workspace.
  *   workspace: workspace_bytes >= fp8_newton_schulz_workspace_bytes(batch, m,
- *           n) of scratch (too small a one is FP8_ERR_SHAPE); its contents
- *           before the call do not matter.  Two calls that may run at the
+ *           n) of scratch (too small a one is FP8_ERR_SHAPE), which is a page
+ *           where every such batch takes one launch; its contents before the
+ *           call do not matter.  Two calls that may run at the
  *           same time need different workspaces.
  * All pointers are 16-byte aligned.  batch == 0 is a no-op.
  */

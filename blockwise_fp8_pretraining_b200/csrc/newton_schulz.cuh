@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_kernel(const T* __restrict_
     if (threadIdx.x == 0) partial[static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = sum;
 }
 
-// Multiplication by scale / norm, as two powers of two and a value in [1, 2), so
+// Multiplication by scale / norm, as two powers of two and a value in [0.5, 1), so
 // that neither a tiny nor a huge norm overflows or loses digits.  A zero norm
 // gives zeros, a non-finite one NaN.
 struct Factor {

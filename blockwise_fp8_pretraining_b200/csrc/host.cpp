@@ -1,7 +1,7 @@
 // The host side of the operators around the linears, for calls on the current
-// stream: the same checks and allocations as the Python binding's, an order of
-// magnitude cheaper.  One token's norm takes 2 us on the GPU and took 15.5 us of
-// Python (four outputs' allocation, a check per tensor, ctypes); here it takes 7.
+// stream: the same checks and allocations as the Python binding's, at less than half
+// the cost.  One token's norm takes 2 us on the GPU and a call of it 15.5 us through
+// Python (four outputs' allocation, a check per tensor, ctypes); 6 to 7 through here.
 //
 // Each function takes its Python counterpart's arguments in order (None where
 // left out) and returns its result, or the C entry point's status as an int, or

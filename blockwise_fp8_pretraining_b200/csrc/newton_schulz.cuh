@@ -48,10 +48,11 @@
 // contraction, where the parts before the last leave their FP32 sums in the
 // workspace and the pair with the last one adds them in order.
 //
-// On a B200, five steps: [12288, 2048] FP32 787 us (1.04 PFLOP/s, the symmetric
+// On a B200, five steps: [12288, 2048] FP32 782 us (1.04 PFLOP/s, the symmetric
 // products' halves counted once; a library product of that size runs at 1.33
-// PFLOP/s on the same data, held by the power limit), [2048, 6144] 470 us, [2048,
-// 2048] 272 us.  A product's stages take 0.30 us each at full clock (the tensor
+// PFLOP/s on the same data, held by the power limit), [2048, 6144] 470 us, [4096,
+// 2048] 378 us, [2048, 2048] 272 us; over a second of runs, the clock then at 1.57
+// GHz, 920, 540, 406 and 272.  A product's stages take 0.30 us each at full clock (the tensor
 // cores' 512 clocks are 0.27); around them stand about 1.5 us until the first
 // operands arrive, 2 to 4 us of epilogue and 1.5 us between kernels, which is
 // what bounds matrices of a few hundred rows ([6, 520, 1100] 195 us, 13 us a

@@ -298,7 +298,8 @@ enum {
  * nothing else gets stats (-inf, 0), entropy 0 and log probabilities -inf.  A
  * NaN or +inf logit makes the row's results NaN; NaN logits are never among
  * the alternatives (where too few others are left, index -1 and NaN).
- * Arithmetic is FP32 in a fixed order, so results repeat run to run.
+ * Arithmetic is FP32 in a fixed order, so results repeat run to run;
+ * probabilities below 2^-126 count as 0, here and in the gradient.
  * Passage: Puro-2B-Base model card (friendli.ai), model property table
  * (vocabulary of 151,936, untied output embedding) and training-setup
  * paragraph (operations other than the linears' products in BF16 or FP32).
